@@ -1,5 +1,6 @@
 /*
- * ltc.h -- C ABI of the MI355X (gfx950) lossless tensor codec.
+ * ltc.h -- C ABI of the MI355X (gfx950) lossless tensor codec and of the
+ * 8-bit key/value cache (its part is at the end).
  *
  * The library compresses the bytes of a tensor of model weights the way
  * ZipNN does ("NOTE-241: ZipNN" (nucleation notes), section "Method",
@@ -445,6 +446,95 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
                               const void* const* h_blob_ptrs, const uint64_t* h_blob_nbytes,
                               void* const* h_dst_ptrs, const uint64_t* h_dst_capacity,
                               int32_t* d_status, hipStream_t stream, const hipEvent_t* h_events);
+
+/* ---------------------------------------------------------------------------
+ * THE 8-BIT KEY/VALUE CACHE.  Keys and values of a served model, quantised as
+ * they are written, read back, and attended to in place.
+ *
+ * The cache is `pages` pages of `page` tokens (16, 32, 64, 128 or 256), each
+ * for `heads` heads of `dim` numbers (64, 96, 128, 192 or 256), with one
+ * power-of-two scale for each page, head and kind (key, value):
+ *   k_codes u8 [pages][heads][page/16][dim/16][16 tokens][16 dims]
+ *   v_codes u8 [pages][heads][page/16][dim][16 tokens]
+ *   scales  u8 [pages][heads][2] (key, value); a scale is 2^(byte - 127), byte 1..254
+ * Codes are OCP E4M3 (LTC_E4M3) or two's-complement integers (LTC_INT8); a
+ * number is its code times its scale.  The layouts are those in which the
+ * matrix cores take 16 tokens of keys and values.
+ *
+ * A call's rows belong to sequences: rows cu[i]..cu[i+1] to sequence i, as its
+ * last positions, lengths[i] - (cu[i+1] - cu[i]) to lengths[i] - 1.  Position t
+ * of a sequence is token t % page of page table[i][t / page].  Without d_cu
+ * every sequence has one row.
+ *
+ * What only the device knows is checked there: a table entry outside
+ * [0, pages) below a sequence's length, and lengths or row offsets that
+ * contradict each other (offsets that decrease or pass `rows`, more rows than
+ * positions, more positions than the table has pages for) set
+ * LTC_CACHE_BAD_PAGE and LTC_CACHE_BAD_SEQUENCE in *d_status and touch nothing
+ * out of bounds: such a page is not written, reads as zeros and is not
+ * attended to; such a sequence is not written, and its rows get zeros.
+ * The status is only ever added to; a caller clears it when it has read it.
+ *
+ * Argument errors that the host sees (types, sizes, null or misaligned
+ * pointers, a grid past the device's limits) return before anything is
+ * enqueued.  A call without rows or sequences succeeds and does nothing. */
+enum { LTC_E4M3 = 0, LTC_INT8 = 1 };
+enum { LTC_CACHE_BAD_PAGE = 1, LTC_CACHE_BAD_SEQUENCE = 2 };
+
+typedef struct {
+  void* d_k_codes;     /* 16-byte aligned, like d_v_codes */
+  void* d_v_codes;
+  void* d_scales;      /* 2-byte aligned */
+  uint32_t* d_status;  /* one word */
+  uint32_t pages, heads, dim, page;
+  int32_t codes;       /* LTC_E4M3 or LTC_INT8 */
+  int32_t dtype;       /* LTC_BF16 or LTC_FP16: keys, values, queries and outputs of the calls */
+} ltc_cache;
+
+typedef struct {
+  const int32_t* d_table;    /* [seqs][width], rows of it table_stride apart */
+  const int32_t* d_lengths;  /* [seqs] */
+  const int32_t* d_cu;       /* [seqs + 1], or NULL: one row per sequence */
+  uint64_t table_stride;
+  uint32_t seqs, rows, width;
+  uint32_t reserved;         /* 0 */
+} ltc_cache_seqs;
+
+/* Rows of 16-bit numbers: element i of a row and head is
+ * d_base[row * row_stride + head * head_stride + i].  16-byte aligned, strides
+ * in elements and multiples of 8. */
+typedef struct {
+  const void* d_base;
+  uint64_t row_stride, head_stride;
+} ltc_cache_rows;
+
+/* Write keys and values [rows][heads][dim] to their positions.  The scale of a
+ * page and head is the smallest power of two, not below 2^-100, for which the
+ * largest magnitude among the page's new rows fits the codes (448 in E4M3, 127
+ * in INT8); a page that holds earlier positions of the sequence keeps its scale
+ * if that is larger, and if it is smaller the earlier tokens' codes are divided
+ * by the growth and rounded again.  Numbers are rounded to the nearest code,
+ * ties to even.  Infinities do not count for the scale and saturate; a NaN
+ * becomes E4M3's NaN, or 0 in INT8.  Tokens behind a sequence's end are left as
+ * they are.  No two sequences of a call may write to the same page. */
+int ltc_cache_write(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* k,
+                    const ltc_cache_rows* v, hipStream_t stream);
+
+/* Read the rows' positions back: d_k and d_v are [rows][heads][dim], 16-byte
+ * aligned, code times scale rounded once. */
+int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k, void* d_v, hipStream_t stream);
+
+/* Attention of queries [rows][q_heads][dim] over the cache, whose last
+ * positions the rows are: the row at position p sees positions t <= p, and with
+ * window > 0 only t > p - window.  Query head h reads head h / (q_heads /
+ * heads).  d_out [rows][q_heads][dim] (16-byte aligned) gets
+ * softmax(scale * q k^T) v, zeros for a row that sees nothing.  The workspace
+ * has ltc_cache_attend_workspace_size() bytes, 256-byte aligned (none may be
+ * needed, then d_ws may be NULL); its contents do not matter. */
+uint64_t ltc_cache_attend_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,
+                                         uint32_t window);
+int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
+                     uint32_t window, float scale, void* d_out, void* d_ws, uint64_t ws_nbytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

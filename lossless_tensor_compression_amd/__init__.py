@@ -18,6 +18,8 @@ API (names as in cuZipNN 0.1.0, "API", and the C ABI):
   compress_delta(t, base) / decompress_delta(blob, base): XOR deltas against
       a base tensor, zero-run coded where the delta is mostly zero bytes
   blob_info / blob_stats for host-side inspection of a blob's header
+  KVCache, cache_write / cache_read / cache_attend: a paged key/value cache in
+      8 bits (kv_cache.py)
 """
 import ctypes
 import os
@@ -110,7 +112,13 @@ def lib():
         L.ltc_crc32_chunks.argtypes = [vp, u64, u32, vp, vp]
         L.ltc_crc32_chunks_batch.argtypes = [i32, pvp, pu64, u32, pvp, vp]
         L.ltc_blob_stats.argtypes = [ctypes.c_char_p, u64, ctypes.POINTER(Stats)]
-        for name in ("ltc_compress_workspace_size", "ltc_compress_batch_workspace_size",
+        L.ltc_cache_write.argtypes = [vp, vp, vp, vp, vp]
+        L.ltc_cache_read.argtypes = [vp, vp, vp, vp, vp]
+        L.ltc_cache_attend_workspace_size.argtypes = [vp, vp, u32, u32]
+        L.ltc_cache_attend_workspace_size.restype = u64
+        L.ltc_cache_attend.argtypes = [vp, vp, vp, u32, u32, ctypes.c_float, vp, vp, u64, vp]
+        for name in ("ltc_cache_write", "ltc_cache_read", "ltc_cache_attend",
+                     "ltc_compress_workspace_size", "ltc_compress_batch_workspace_size",
                      "ltc_compress", "ltc_compress_noalloc", "ltc_compress_batch",
                      "ltc_compress_batch_prof",
                      "ltc_compress_with_crc32", "ltc_compress_batch_with_crc32", "ltc_compress_batch_ex",
@@ -572,3 +580,6 @@ def blob_stats(blob):
         "group_percent": [100.0 * st.payload_bytes[k] / st.stream_bytes[k]
                           if st.stream_bytes[k] else 0.0 for k in range(e)],
     }
+
+
+from .kv_cache import KVCache, cache_attend, cache_read, cache_write  # noqa: E402,F401

@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libltc.so")
 BUILD = os.path.join(ROOT, "_build")
-SOURCES = ["ltc_compress.hip", "ltc_decompress.hip", "ltc_crc32.hip", "ltc_api.hip"]
+SOURCES = ["ltc_compress.hip", "ltc_decompress.hip", "ltc_crc32.hip", "ltc_api.hip",
+           "ltc_cache_store.hip", "ltc_cache_attend.hip", "ltc_cache_api.hip"]
 # plain C++ (no device code): the host-side parsing of blob bytes
 HOST_SOURCES = ["ltc_host.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -57,7 +58,7 @@ def _compile_host(src: str, verbose: bool) -> str:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=4) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=8) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     objs += [_compile_host(s, verbose) for s in HOST_SOURCES]
     tmp = OUT + ".tmp"

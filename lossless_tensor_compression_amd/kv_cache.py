@@ -1,0 +1,192 @@
+"""A paged key/value cache in 8 bits: quantised as it is written, read back,
+and attended to in place.
+
+  KVCache.empty(...) / KVCache.of(...)  the cache's tensors and their layout
+  cache_write(cache, k, v, table, lengths, cu)   new keys and values to their positions
+  cache_read(cache, table, lengths, cu, rows)    positions back as 16-bit rows
+  cache_attend(cache, q, table, lengths, cu)     attention of new queries
+
+A binding over ltc_cache_write, ltc_cache_read and ltc_cache_attend of
+include/ltc.h, where the layouts, the rounding and what happens with bad
+tables are written down.  Calls run on the current stream, allocate nothing
+but their outputs and workspace, and never synchronise, so they can be
+captured in a graph.
+
+Rows cu[i]..cu[i+1] of a call belong to sequence i and stand for its last
+positions, lengths[i] - (cu[i+1] - cu[i]) to lengths[i] - 1; without cu each
+sequence has one row.  Position t of sequence i is token t % page of page
+table[i, t // page].  table, lengths and cu are int32 tensors on the GPU.
+"""
+import ctypes
+import struct
+
+import torch
+
+from . import LTCError, _check, lib
+
+E4M3, INT8 = 0, 1
+CODES = {"e4m3": E4M3, "int8": INT8}
+CACHE_DTYPES = {torch.bfloat16: 1, torch.float16: 2}
+PAGES = (16, 32, 64, 128, 256)
+DIMS = (64, 96, 128, 192, 256)
+BAD_PAGE, BAD_SEQUENCE = 1, 2
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds a Stream object: 2.7 us a call
+_pack_seqs = struct.Struct("=QQQQIIII").pack      # ltc_cache_seqs
+_pack_rows = struct.Struct("=QQQ").pack           # ltc_cache_rows
+
+
+class CacheStruct(ctypes.Structure):
+    _fields_ = [("d_k_codes", ctypes.c_void_p), ("d_v_codes", ctypes.c_void_p), ("d_scales", ctypes.c_void_p),
+                ("d_status", ctypes.c_void_p), ("pages", ctypes.c_uint32), ("heads", ctypes.c_uint32),
+                ("dim", ctypes.c_uint32), ("page", ctypes.c_uint32), ("codes", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class KVCache:
+    """The tensors of a cache and what the library has to know of them.
+
+    k_codes uint8 [pages, heads, page/16, dim/16, 16 tokens, 16 dims]
+    v_codes uint8 [pages, heads, page/16, dim, 16 tokens]
+    scales  uint8 [pages, heads, 2], a scale is 2^(byte - 127)
+    dtype: torch.bfloat16 or torch.float16, of keys, values, queries and
+    outputs; codes: "e4m3" or "int8"."""
+
+    def __init__(self, k_codes, v_codes, scales, dtype, codes):
+        if codes not in CODES:
+            raise LTCError(-2, f"codes {codes!r}")
+        if dtype not in CACHE_DTYPES:
+            raise LTCError(-2, f"dtype {dtype}")
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes), ("scales", scales)):
+            if not t.is_cuda or t.device != k_codes.device:
+                raise ValueError(f"{name} must be on the cache's GPU")
+            if t.dtype != torch.uint8 or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous uint8")
+        pages, heads, page, dim = self._shape(k_codes, v_codes, scales)
+        self.k_codes, self.v_codes, self.scales = k_codes, v_codes, scales
+        self.pages, self.heads, self.page, self.dim = pages, heads, page, dim
+        self.dtype, self.codes, self.device = dtype, codes, k_codes.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=k_codes.device)
+        self._lib = lib()
+        self._struct = CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), scales.data_ptr(), self.status.data_ptr(),
+                                   pages, heads, dim, page, CODES[codes], CACHE_DTYPES[dtype])
+        self._ref = ctypes.byref(self._struct)
+        self._index = self.device.index
+
+    @staticmethod
+    def _shape(k_codes, v_codes, scales):
+        if k_codes.dim() != 6 or k_codes.shape[4:] != (16, 16):
+            raise ValueError("k_codes must be [pages, heads, page/16, dim/16, 16, 16]")
+        pages, heads, blocks, parts = k_codes.shape[:4]
+        if v_codes.shape != (pages, heads, blocks, parts * 16, 16):
+            raise ValueError("v_codes must be [pages, heads, page/16, dim, 16]")
+        if scales.shape != (pages, heads, 2):
+            raise ValueError("scales must be [pages, heads, 2]")
+        if blocks * 16 not in PAGES:
+            raise ValueError(f"a page must have one of {PAGES} tokens")
+        if parts * 16 not in DIMS:
+            raise ValueError(f"a head must have one of {DIMS} dims")
+        if heads < 1:
+            raise ValueError("at least one head")
+        return pages, heads, blocks * 16, parts * 16
+
+    @classmethod
+    def of(cls, k_codes, v_codes, scales, dtype=torch.bfloat16, codes="e4m3"):
+        """A cache over tensors that the caller holds."""
+        return cls(k_codes, v_codes, scales, dtype, codes)
+
+    @classmethod
+    def empty(cls, pages, heads, dim, page=64, dtype=torch.bfloat16, codes="e4m3", device="cuda"):
+        """A cache with tensors of its own, zeros with the lowest scale."""
+        if page not in PAGES or dim not in DIMS:
+            raise ValueError(f"page must be one of {PAGES} and dim one of {DIMS}")
+        return cls(torch.zeros((pages, heads, page // 16, dim // 16, 16, 16), dtype=torch.uint8, device=device),
+                   torch.zeros((pages, heads, page // 16, dim, 16), dtype=torch.uint8, device=device),
+                   torch.full((pages, heads, 2), 27, dtype=torch.uint8, device=device), dtype, codes)
+
+    def check(self):
+        """Raises if a call since the last check met a bad page or sequence
+        (waits for the GPU)."""
+        bits = int(self.status.item())
+        self.status.zero_()
+        if bits:
+            what = [n for b, n in ((BAD_PAGE, "a table entry outside the cache"),
+                                   (BAD_SEQUENCE, "lengths or cu that contradict each other")) if bits & b]
+            raise LTCError(-5, " and ".join(what))
+
+    def _seqs(self, table, lengths, cu, rows):
+        """ltc_cache_seqs as bytes; what can be seen without the GPU is checked."""
+        seqs = lengths.numel()
+        for name, t in (("table", table), ("lengths", lengths), ("cu", cu)):
+            if t is not None and (t.dtype != torch.int32 or t.get_device() != self._index):
+                raise ValueError(f"{name} must be int32 on the cache's GPU")
+        if table.dim() != 2 or table.shape[0] != seqs or lengths.dim() != 1:
+            raise ValueError("table must be [sequences, pages] and lengths [sequences]")
+        if not lengths.is_contiguous() or (table.stride(1) != 1 and table.shape[1] > 1):
+            raise ValueError("lengths and the rows of table must be contiguous")
+        if cu is None:
+            if rows != seqs:
+                raise ValueError("without cu there is one row for each sequence")
+        elif cu.dim() != 1 or cu.numel() != seqs + 1 or not cu.is_contiguous():
+            raise ValueError("cu must be contiguous [sequences + 1]")
+        width = table.shape[1]
+        stride = table.stride(0) if seqs > 1 else width
+        if stride < width:
+            raise ValueError("the rows of table must not overlap")
+        return _pack_seqs(table.data_ptr(), lengths.data_ptr(), 0 if cu is None else cu.data_ptr(), stride,
+                          seqs, rows, width, 0)
+
+    def _rows(self, t, heads, name):
+        """t as rows that the kernels can take (a copy where its strides or
+        alignment do not let them) and its ltc_cache_rows as bytes."""
+        if t.dtype != self.dtype or t.get_device() != self._index:
+            raise ValueError(f"{name} must be {self.dtype} on the cache's GPU")
+        if t.dim() != 3 or t.shape[2] != self.dim or (heads is not None and t.shape[1] != heads):
+            raise ValueError(f"{name} must be [rows, {'heads' if heads is None else heads}, {self.dim}]")
+        r, h, d = t.stride()
+        if d != 1 or r % 8 or h % 8 or t.data_ptr() % 16:
+            t = t.contiguous() if not t.is_contiguous() else t.clone()
+            r, h, d = t.stride()
+        return t, _pack_rows(t.data_ptr(), r, h)
+
+
+def cache_write(cache, k, v, table, lengths, cu=None):
+    """Quantises keys and values [rows, heads, dim] into the cache's pages."""
+    k, kr = cache._rows(k, cache.heads, "k")
+    v, vr = cache._rows(v, cache.heads, "v")
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("one value row for each key row")
+    s = cache._seqs(table, lengths, cu, k.shape[0])
+    _check(cache._lib.ltc_cache_write(cache._ref, s, kr, vr, _raw_stream(cache._index)), "cache_write")
+
+
+def cache_read(cache, table, lengths, cu=None, rows=None):
+    """The keys and values (two tensors [rows, heads, dim] of the cache's
+    dtype) at the positions of the call's rows; rows = cu[-1], which only the
+    GPU knows, has to be given with cu."""
+    if rows is None:
+        if cu is not None:
+            raise ValueError("rows must be given with cu")
+        rows = lengths.numel()
+    s = cache._seqs(table, lengths, cu, rows)
+    k = torch.empty((rows, cache.heads, cache.dim), dtype=cache.dtype, device=cache.device)
+    v = torch.empty_like(k)
+    _check(cache._lib.ltc_cache_read(cache._ref, s, k.data_ptr(), v.data_ptr(), _raw_stream(cache._index)),
+           "cache_read")
+    return k, v
+
+
+def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None):
+    """softmax(scale * q k^T) v of queries [rows, q_heads, dim] over the
+    positions up to each row's own (with window: the last `window` of them);
+    zeros for a row that sees nothing.  scale is dim^-0.5 by default."""
+    q, qr = cache._rows(q, None, "q")
+    rows, q_heads, dim = q.shape
+    s = cache._seqs(table, lengths, cu, rows)
+    out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
+    need = cache._lib.ltc_cache_attend_workspace_size(cache._ref, s, q_heads, window)
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _check(cache._lib.ltc_cache_attend(cache._ref, s, qr, q_heads, window, dim ** -0.5 if scale is None else scale,
+                                       out.data_ptr(), ws.data_ptr() if need else None, need,
+                                       _raw_stream(cache._index)), "cache_attend")
+    return out
