@@ -1,82 +1,546 @@
 // ltc_cache_attend.hip -- attention of new queries over the 8-bit cache.
+//
+// One pass over the positions with the softmax's running maximum and sum.
+// Per head, with x_t = log2(e) scale (q . k_t) and 2^w the scale of token t's
+// values (its page's):
+//   out = sum_t 2^(x_t) 2^w c_t / sum_t 2^(x_t),   c_t the value's codes.
+// The weights u_t = 2^(x_t + w - m) carry the values' scale, m is a running
+// bound of x_t + w (not below its maximum by more than kSlack), and the sum
+// below the fraction gathers u_t 2^-w: so the weights that multiply the codes
+// stay near one whatever the pages' scales are, and the codes go into the
+// matrix cores as they are.
 #include "ltc_cache_device.h"
 
 namespace ltc {
 namespace {
 
-constexpr int kMaxDim = 256;
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef float float2v __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
 
-// One wave for a row and query head: one pass over the positions it sees with
-// the running maximum and sum of the softmax; lanes over the head's dims.
-template <bool E4M3, int DT>
-__global__ __launch_bounds__(64) void k_cache_attend(CacheView c, SeqView s, AttendArgs a) {
-  const uint32_t row = blockIdx.x, qh = blockIdx.y, lane = threadIdx.x;
-  const uint32_t head = qh / (a.q_heads / c.heads);
-  const UnitMap map{1, 1, 0};
+constexpr float kLog2e = 1.4426950408889634f;
+// A tile whose largest x + w is within 2^kSlack of the running bound keeps the
+// bound: weights up to 2^kSlack are as exact in fp16 as those up to 1, and the
+// accumulators are seldom scaled.
+constexpr float kSlack = 6.0f;
+
+// Eight codes (two dwords) as fp16, exactly: E4M3 has 3 bits of mantissa and
+// exponents down to 2^-9, INT8 7 bits.
+template <bool E4M3> __device__ __forceinline__ half8 codes_to_half(uint32_t a, uint32_t b) {
+  union {
+    half8 h8;
+    half2v h2[4];
+    uint32_t u[4];
+  } r;
+  if constexpr (E4M3) {
+    r.h2[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)a, 1.0f, false);
+    r.h2[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)a, 1.0f, true);
+    r.h2[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b, 1.0f, false);
+    r.h2[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b, 1.0f, true);
+  } else {
+    // 0x6400 | u is 1024 + u in fp16; u = code + 128
+    a ^= 0x80808080u;
+    b ^= 0x80808080u;
+    r.u[0] = __builtin_amdgcn_perm(0x64646464u, a, 0x04010400u);
+    r.u[1] = __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u);
+    r.u[2] = __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u);
+    r.u[3] = __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u);
+    const half2v off = {(_Float16)1152, (_Float16)1152};
+    for (int i = 0; i < 4; ++i) r.h2[i] -= off;
+  }
+  return r.h8;
+}
+
+// Whether any of four E4M3 codes is a NaN (0x7f or 0xff).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
+  return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// Of the bytes at positions t..t+3, those in [lo, hi) as 0xff.
+__device__ __forceinline__ uint32_t byte_mask(int t, int lo, int hi) {
+  const int a = min(max(lo - t, 0), 4), b = min(max(hi - t, 0), 4);
+  const uint32_t below_b = (uint32_t)((1ull << (8 * b)) - 1), below_a = (uint32_t)((1ull << (8 * a)) - 1);
+  return below_b & ~below_a;
+}
+
+// The positions that a tile of packed rows looks at, in steps of kStep, and
+// how they are shared out: split i takes steps [i * per, (i + 1) * per).
+constexpr int kStep = 64;
+struct Range {
+  int lo, hi;            // positions [lo, hi) that some row sees
+  int first, steps;      // steps first .. first + steps cover them
+  int per, used;         // steps of a split, splits with work
+};
+
+__device__ __forceinline__ Range range_of(const Span& sp, uint32_t tok0, uint32_t tok1, uint32_t window,
+                                          uint32_t splits, int least) {
+  Range r;
+  r.hi = (int)(sp.start + tok1);
+  r.lo = (int)(sp.start + tok0) + 1 - (int)window;
+  if (!window || r.lo < 0) r.lo = 0;
+  r.first = r.lo / kStep;
+  r.steps = (r.hi + kStep - 1) / kStep - r.first;
+  r.per = max(least, (int)((r.steps + splits - 1) / splits));
+  r.used = (r.steps + r.per - 1) / r.per;
+  return r;
+}
+
+// partial results of a split: [unit][head][split][row of the tile] numerators
+// (dim floats), then bound and sum (2 floats) in an array behind them
+__device__ __forceinline__ uint64_t partial_at(uint32_t unit, uint32_t heads, uint32_t head, uint32_t splits,
+                                               uint32_t split, uint32_t rows) {
+  return ((((uint64_t)unit * heads + head) * splits) + split) * rows;
+}
+
+template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return (uint32_t)narrow<DT>(a) | (uint32_t)narrow<DT>(b) << 16;
+}
+__device__ __forceinline__ uint32_t pack2(bool bf16, float a, float b) {
+  return bf16 ? pack2<LTC_BF16>(a, b) : pack2<LTC_FP16>(a, b);
+}
+
+// waves for each SIMD that the kernel's registers are to leave room for
+constexpr int rows_occupancy(int D, int NC) { return D * NC <= 128 ? 3 : D * NC <= 256 && D < 256 ? 2 : 1; }
+
+// W waves on a tile of 16 * NC packed rows (row r of a sequence and key head
+// is token r / G, query head r % G of the head's G) and one split of its
+// positions; each wave takes every W-th step of 64 tokens, from memory into
+// registers with nothing in between.  Lane l = 16 g + n of a wave:
+//  - S^T = K Q^T (16x16x32, fp16 in, fp32 out) in four blocks b: row m of the
+//    product is token 16 (m / 4) + 4 b + m % 4 of the step, so the lane, which
+//    gets rows 4 g + i, holds the scores of tokens 16 g + 4 b + i against row n:
+//    16 tokens in a row, all of one page, so the page's scales are the lane's;
+//  - O^T = V^T P^T: the lane's 16 bytes of value codes of a dim are those same
+//    tokens, so the weights go from the first product's registers into the
+//    second's, rounded to fp16, with no move between lanes.
+// Keys are read 16 dims of a token a lane (k may come in any order, as long as
+// Q's does too), values 16 tokens of a dim a lane; a load instruction covers
+// whole 64- and 256-byte runs.  The next step's keys are loaded once this
+// step's are used up, and so for values, so one step (2 * 64 * D bytes) is in
+// flight for each wave.
+template <bool E4M3, int D, int NC, int W>
+__global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16,
+                                                         uint32_t splits) {
+  constexpr int R = 16 * NC, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
+  __shared__ float lds_acc[W][16][D + 4];
+  __shared__ float lds_m[W][R], lds_l[W][R];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const uint32_t unit = blockIdx.x / splits, split = blockIdx.x % splits, head = blockIdx.y;
+  const uint32_t G = a.q_heads / c.heads;
   uint32_t seq;
   Span sp;
   uint64_t own;
-  const bool mine = locate_unit(c, s, map, row, WaveCount{s, map, row}, &seq, &sp, &own) && own < sp.n;
-  if (!sp.ok && lane == 0) report(c, kCacheBadSeq);
-  constexpr int N = kMaxDim / 64;
-  float q[N], acc[N];
-  for (int i = 0; i < N; ++i) {
-    const uint32_t d = i * 64 + lane;
-    q[i] = d < c.dim ? widen<DT>(a.q.base[row * a.q.row_stride + qh * a.q.head_stride + d]) * a.scale : 0.0f;
-    acc[i] = 0.0f;
+  const bool mine = locate_unit(c, s, map, unit, WaveCount{s, map, unit}, &seq, &sp, &own);
+  if (!sp.ok && threadIdx.x == 0) report(c, kCacheBadSeq);
+  const uint32_t packed = sp.n * G;
+  if (!mine || own * R >= packed) return;
+  const uint32_t r0 = (uint32_t)own * R, r1 = min(r0 + R, packed);
+  Range rg = range_of(sp, r0 / G, (r1 - 1) / G + 1, a.window, splits, W);
+  if (!sp.ok || c.pages == 0) {
+    if (sp.ok && threadIdx.x == 0) report(c, kCacheBadPage);
+    rg.hi = rg.lo = rg.steps = rg.used = 0;
   }
-  float m = -INFINITY, sum = 0.0f;
-  if (sp.ok && mine) {
-    const uint32_t end = sp.start + (uint32_t)own + 1;
-    uint32_t t = a.window && end > a.window ? end - a.window : 0;
-    for (; t < end; ++t) {
-      uint32_t page;
-      if (!page_at(s, seq, t >> c.page_log, c.pages, &page)) {
-        if (lane == 0) report(c, kCacheBadPage);
-        continue;
-      }
-      const uint8_t* kc = c.k + head_offset(c, page, head);
-      const uint8_t* vc = c.v + head_offset(c, page, head);
-      const uint8_t* scales = c.scales + ((uint64_t)page * c.heads + head) * 2;
-      const float ks = power_of_two(scales[0] - 127), vs = power_of_two(scales[1] - 127);
-      const uint32_t o = t & ((1u << c.page_log) - 1);
-      float x = 0.0f;
-      for (int i = 0; i < N; ++i) {
-        const uint32_t d = i * 64 + lane;
-        if (d < c.dim) x += q[i] * code_value<E4M3>(kc[k_code(o, d, c.dim)]);
-      }
-      for (int w = 32; w; w >>= 1) x += __shfl_xor(x, w);
-      x *= ks;
-      const float top = fmaxf(m, x), keep = expf(m - top), p = expf(x - top);
-      m = top;
-      sum = sum * keep + p;
-      for (int i = 0; i < N; ++i) {
-        const uint32_t d = i * 64 + lane;
-        acc[i] = acc[i] * keep + (d < c.dim ? p * (code_value<E4M3>(vc[v_code(o, d, c.dim)]) * vs) : 0.0f);
-      }
+  if ((int)split >= max(rg.used, 1)) return;
+
+  // queries: lane (n, g) holds row n's dims of k-group g
+  half8 q[NC][KS];
+  float factor[NC];
+  int row_lo[NC], row_hi[NC];
+  for (int nc = 0; nc < NC; ++nc) {
+    const uint32_t r = r0 + nc * 16 + n;
+    const bool live = r < packed;
+    const uint32_t token = live ? r / G : 0, qh = head * G + (live ? r % G : 0);
+    const uint16_t* src = a.q.base + (uint64_t)(sp.row0 + token) * a.q.row_stride + (uint64_t)qh * a.q.head_stride;
+    row_hi[nc] = live ? (int)(sp.start + token) + 1 : 0;
+    row_lo[nc] = a.window ? max(row_hi[nc] - (int)a.window, 0) : 0;
+    uint4v raw[KS];
+    for (int x = 0; x < KS; ++x) {
+      const int d = x < 2 * KL ? (4 * (x / 2) + g) * 16 + (x & 1) * 8 : 64 * KL + g * 8;
+      raw[x] = live ? *reinterpret_cast<const uint4v*>(src + d) : uint4v{0, 0, 0, 0};
+    }
+    factor[nc] = a.scale * kLog2e;
+    if (bf16) {
+      // to fp16 by a power of two that brings the row's largest number to
+      // 2^14..2^15: what is lost is below 2^-39 of it, less than the sum's
+      // own rounding in fp32
+      uint32_t top = 0;
+      for (int x = 0; x < KS; ++x)
+        for (int i = 0; i < 4; ++i) top = max(top, max(raw[x][i] & 0x7fffu, (raw[x][i] >> 16) & 0x7fffu));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+      const int e = (int)(top >> 7);  // biased exponent; 255: infinities or NaN, which no factor helps
+      const int up = e == 255 ? 0 : min(141 - e, 127);
+      factor[nc] *= power_of_two(-up);
+      const float f = power_of_two(up);
+      for (int x = 0; x < KS; ++x)
+        for (int i = 0; i < 4; ++i) {
+          q[nc][x][2 * i] = (_Float16)(widen<LTC_BF16>(raw[x][i] & 0xffffu) * f);
+          q[nc][x][2 * i + 1] = (_Float16)(widen<LTC_BF16>(raw[x][i] >> 16) * f);
+        }
+    } else {
+      for (int x = 0; x < KS; ++x) q[nc][x] = __builtin_bit_cast(half8, raw[x]);
     }
   }
-  for (int i = 0; i < N; ++i) {
-    const uint32_t d = i * 64 + lane;
-    if (d < c.dim) a.out[((uint64_t)row * a.q_heads + qh) * c.dim + d] = narrow<DT>(sum == 0.0f ? 0.0f : acc[i] / sum);
+
+  float4v acc[NC][DB];
+  float m[NC], l[NC];
+  for (int nc = 0; nc < NC; ++nc) {
+    m[nc] = -INFINITY;
+    l[nc] = 0.0f;
+    for (int i = 0; i < DB; ++i) acc[nc][i] = float4v{0, 0, 0, 0};
   }
+  // positions that every row sees need no masks
+  const int all_lo = a.window ? max((int)(sp.start + (r1 - 1) / G) + 1 - (int)a.window, 0) : 0;
+  const int all_hi = (int)(sp.start + r0 / G) + 1;
+
+  const int step_end = rg.first + min((int)(split + 1) * rg.per, rg.steps);
+  int step = rg.first + (int)split * rg.per + wave;
+
+  const uint32_t page_mask = (1u << c.page_log) - 1;
+  const int kb = n >> 2;  // the block whose tokens' keys this lane reads
+  const int32_t* table = s.table + seq * s.table_stride;
+  // byte offset of the 16 tokens at t within k or v, and whether they have a page
+  auto block_at = [&](int t, bool* have) -> uint64_t {
+    const bool want = t < rg.hi;
+    const int32_t p = want ? table[(uint32_t)t >> c.page_log] : -1;
+    *have = (uint32_t)p < c.pages;
+    return head_offset(c, *have ? (uint32_t)p : 0, head) + (((uint32_t)t & page_mask) >> 4) * (16 * D);
+  };
+  uint4v kr[4][KL], vr[DB];
+  uint2v kt[4];
+  uint32_t scales;
+  bool have_v, next_have_v = false;
+  auto load_k = [&](uint64_t off) {
+    const uint8_t* p = c.k + off + g * 256 + (n & 3) * 16;
+    for (int b = 0; b < 4; ++b)
+      for (int j = 0; j < KL; ++j) kr[b][j] = *reinterpret_cast<const uint4v*>(p + j * 1024 + b * 64);
+    if constexpr (TAIL) {
+      const uint8_t* pt = c.k + off + KL * 1024 + (g >> 1) * 256 + (n & 3) * 16 + (g & 1) * 8;
+      for (int b = 0; b < 4; ++b) kt[b] = *reinterpret_cast<const uint2v*>(pt + b * 64);
+    }
+  };
+  auto load_v = [&](uint64_t off) {
+    const uint8_t* p = c.v + off + n * 16;
+    for (int i = 0; i < DB; ++i) vr[i] = *reinterpret_cast<const uint4v*>(p + i * 256);
+  };
+  auto load_scales = [&](int t, bool have) -> uint32_t {
+    const int32_t p = have ? table[(uint32_t)t >> c.page_log] : 0;
+    return *reinterpret_cast<const uint16_t*>(c.scales + ((uint64_t)p * c.heads + head) * 2);
+  };
+
+  bool have_k;
+  uint64_t v_off = 0;
+  if (step < step_end) {
+    const uint64_t k_off = block_at(step * kStep + kb * 16, &have_k);
+    v_off = block_at(step * kStep + g * 16, &next_have_v);
+    load_k(k_off);
+    load_v(v_off);
+    scales = load_scales(step * kStep + g * 16, next_have_v);
+  }
+  for (; step < step_end; step += W) {
+    const int t0 = step * kStep, tv = t0 + g * 16;
+    have_v = next_have_v;
+    const uint32_t sc = scales;
+    // ---- S^T
+    float4v st[NC][4];
+    for (int nc = 0; nc < NC; ++nc)
+      for (int b = 0; b < 4; ++b) st[nc][b] = float4v{0, 0, 0, 0};
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        const half8 k8 = x < 2 * KL ? codes_to_half<E4M3>(kr[b][x / 2][(x & 1) * 2], kr[b][x / 2][(x & 1) * 2 + 1])
+                                    : codes_to_half<E4M3>(kt[b][0], kt[b][1]);
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+          st[nc][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, q[nc][x], st[nc][b], 0, 0, 0);
+      }
+    const int next = step + W;
+    uint64_t next_v = v_off;
+    if (next < step_end) {
+      const uint64_t k_off = block_at(next * kStep + kb * 16, &have_k);
+      next_v = block_at(next * kStep + g * 16, &next_have_v);
+      load_k(k_off);
+      scales = load_scales(next * kStep + g * 16, next_have_v);
+    }
+    // ---- weights
+    const bool lost = tv < rg.hi && tv + 16 > rg.lo && !have_v;
+    if (lost && n == 0) report(c, kCacheBadPage);
+    const bool edge = t0 < all_lo || t0 + kStep > all_hi || __any(lost);
+    const float ks = power_of_two((int)(sc & 0xff) - 127);
+    const int we = (int)(sc >> 8) - 127;
+    const float w = (float)we;
+    half8 p[NC][2];
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc) {
+      const float f = factor[nc] * ks;
+      if (edge) {
+        for (int b = 0; b < 4; ++b)
+          for (int i = 0; i < 4; ++i) {
+            const int t = tv + 4 * b + i;
+            const bool seen = t >= row_lo[nc] && t < row_hi[nc] && have_v;
+            // hidden: far below everything, but no infinity, so that no
+            // difference of infinities arises
+            st[nc][b][i] = seen ? fmaf(st[nc][b][i], f, w) : -INFINITY;
+          }
+      } else {
+        for (int b = 0; b < 4; ++b)
+          for (int i = 0; i < 4; ++i) st[nc][b][i] = fmaf(st[nc][b][i], f, w);
+      }
+      float top = st[nc][0][0];
+      for (int b = 0; b < 4; ++b)
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, st[nc][b][i]);
+      if (__any(top > m[nc] + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float now = fmaxf(m[nc], top);
+        const float keep = now == m[nc] ? 1.0f : __builtin_amdgcn_exp2f(m[nc] - now);
+        m[nc] = now;
+        l[nc] *= keep;
+        for (int i = 0; i < DB; ++i) acc[nc][i] *= keep;
+      }
+      const float bound = m[nc] == -INFINITY ? 0.0f : m[nc];  // nothing seen yet: every weight is 0
+      float sum = 0.0f;
+      for (int b = 0; b < 4; ++b)
+        for (int i = 0; i < 4; ++i) {
+          const float u = __builtin_amdgcn_exp2f(st[nc][b][i] - bound);
+          sum += u;
+          p[nc][b >> 1][(b & 1) * 4 + i] = (_Float16)u;
+        }
+      l[nc] += __builtin_amdgcn_ldexpf(sum, -we);
+    }
+    // ---- O^T
+    if (edge) {
+      // codes that no row sees may be anything, and 0 * NaN is NaN
+      for (int dw = 0; dw < 4; ++dw) {
+        const uint32_t keep = have_v ? byte_mask(tv + 4 * dw, rg.lo, rg.hi) : 0;
+        for (int i = 0; i < DB; ++i) vr[i][dw] &= keep;
+      }
+      if constexpr (E4M3) {
+        // a NaN that some rows see and others do not: those that do get it
+        // from a product of indicators, and the codes lose it
+        uint32_t any = 0;
+        for (int i = 0; i < DB; ++i)
+          for (int dw = 0; dw < 4; ++dw) any |= nan_bytes(vr[i][dw]);
+        if (__any(any != 0)) {
+          for (int nc = 0; nc < NC; ++nc) {
+            half8 ind[2];
+            for (int b = 0; b < 4; ++b)
+              for (int i = 0; i < 4; ++i) {
+                const int t = tv + 4 * b + i;
+                ind[b >> 1][(b & 1) * 4 + i] = (_Float16)(t >= row_lo[nc] && t < row_hi[nc] && have_v ? 1.0f : 0.0f);
+              }
+            uint64_t hits = 0;
+#pragma unroll 1
+            for (int i = 0; i < DB; ++i) {  // a loop over memory: rare, and it must not cost registers
+              uint4v x = *reinterpret_cast<const uint4v*>(c.v + v_off + n * 16 + i * 256);
+              float4v hit = {0, 0, 0, 0};
+              for (int h = 0; h < 2; ++h) {
+                half8 is;
+                for (int j = 0; j < 8; ++j)
+                  is[j] = (_Float16)((nan_bytes(x[2 * h + j / 4]) >> (8 * (j & 3) + 7)) & 1 ? 1.0f : 0.0f);
+                hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(is, ind[h], hit, 0, 0, 0);
+              }
+              for (int j = 0; j < 4; ++j) hits |= (uint64_t)(hit[j] > 0.0f) << (4 * i + j);
+            }
+            for (int i = 0; i < DB; ++i)
+              for (int j = 0; j < 4; ++j)
+                if (hits >> (4 * i + j) & 1) acc[nc][i][j] = __builtin_nanf("");
+          }
+          for (int dw = 0; dw < 4; ++dw) {
+            const uint32_t keep = have_v ? byte_mask(tv + 4 * dw, rg.lo, rg.hi) : 0;
+            for (int i = 0; i < DB; ++i) {
+              const uint32_t x = *reinterpret_cast<const uint32_t*>(c.v + v_off + n * 16 + i * 256 + dw * 4) & keep;
+              vr[i][dw] = x & ~((nan_bytes(x) >> 7) * 0xffu);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const half8 v8 = codes_to_half<E4M3>(vr[i][2 * h], vr[i][2 * h + 1]);
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+          acc[nc][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p[nc][h], acc[nc][i], 0, 0, 0);
+      }
+    v_off = next_v;
+    if (next < step_end) load_v(v_off);
+  }
+
+  // ---- the waves' parts together
+  for (int nc = 0; nc < NC; ++nc) {
+    l[nc] += __shfl_xor(l[nc], 16);
+    l[nc] += __shfl_xor(l[nc], 32);
+    if (g == 0) {
+      lds_m[wave][nc * 16 + n] = m[nc];
+      lds_l[wave][nc * 16 + n] = l[nc];
+    }
+  }
+  __syncthreads();
+  float* part = static_cast<float*>(a.ws);
+  const uint64_t units = (uint64_t)gridDim.x / splits;
+  float* part_ml = part + units * c.heads * splits * R * D;
+  const uint64_t at = partial_at(unit, c.heads, head, splits, split, R);
+  for (int nc = 0; nc < NC; ++nc) {
+    {
+      const int r = nc * 16 + n;
+      float top = -INFINITY;
+      for (int v = 0; v < W; ++v) top = fmaxf(top, lds_m[v][r]);
+      const float keep = m[nc] == top ? 1.0f : __builtin_amdgcn_exp2f(m[nc] - top);
+      for (int i = 0; i < DB; ++i) {
+        const float4v x = acc[nc][i] * keep;
+        *reinterpret_cast<float4v*>(&lds_acc[wave][n][i * 16 + 4 * g]) = x;
+      }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < 16 * D / 4; x += 64 * W) {
+      const int row = x / (D / 4), d = x % (D / 4) * 4, r = nc * 16 + row;
+      float4v sum = {0, 0, 0, 0};
+      for (int v = 0; v < W; ++v) sum += *reinterpret_cast<const float4v*>(&lds_acc[v][row][d]);
+      float top = -INFINITY, below = 0.0f;
+      for (int v = 0; v < W; ++v) top = fmaxf(top, lds_m[v][r]);
+      for (int v = 0; v < W; ++v)
+        below += lds_l[v][r] * (lds_m[v][r] == top ? 1.0f : __builtin_amdgcn_exp2f(lds_m[v][r] - top));
+      if (rg.used > 1) {
+        *reinterpret_cast<float4v*>(part + (at + r) * D + d) = sum;
+        if (d == 0) *reinterpret_cast<float2v*>(part_ml + (at + r) * 2) = float2v{top, below};
+      } else if (r0 + r < packed) {
+        const uint32_t token = (r0 + r) / G, qh = head * G + (r0 + r) % G;
+        const float inv = below == 0.0f ? 0.0f : 1.0f / below;
+        const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * inv;
+        uint2v packed16 = {pack2(bf16, o[0], o[1]), pack2(bf16, o[2], o[3])};
+        *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = packed16;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the splits of a row, in their order: one workgroup of 256 for a
+// packed row of a tile, D / 4 lanes for its dims, the rest of them for every
+// 1024 / D-th split.
+template <int D>
+__global__ __launch_bounds__(256) void k_attend_join(CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16,
+                                                     uint32_t splits, uint32_t R, uint32_t units, int least) {
+  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+  __shared__ float4v lds[GROUPS][LANES];
+  __shared__ float lds_l[GROUPS];
+  const uint32_t unit = blockIdx.x / R, r = blockIdx.x % R, head = blockIdx.y, G = a.q_heads / c.heads;
+  uint32_t seq;
+  Span sp;
+  uint64_t own;
+  const bool mine = locate_unit(c, s, map, unit, WaveCount{s, map, unit}, &seq, &sp, &own);
+  const uint32_t packed = sp.n * G;
+  if (!mine || !sp.ok || c.pages == 0 || own * R + r >= packed) return;
+  const uint32_t r0 = (uint32_t)own * R, r1 = min(r0 + R, packed);
+  const Range rg = range_of(sp, r0 / G, (r1 - 1) / G + 1, a.window, splits, least);
+  if (rg.used <= 1) return;
+  const float* part = static_cast<const float*>(a.ws);
+  const float* part_ml = part + (uint64_t)units * c.heads * splits * R * D;
+  const uint64_t at = partial_at(unit, c.heads, head, splits, 0, R) + r;
+  float top = -INFINITY;
+  for (int i = threadIdx.x & 63; i < rg.used; i += 64) top = fmaxf(top, part_ml[(at + (uint64_t)i * R) * 2]);
+  for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+  const int grp = threadIdx.x / LANES, x = threadIdx.x % LANES;
+  float4v sum = {0, 0, 0, 0};
+  float below = 0.0f;
+  if (grp < GROUPS) {
+    for (int i = grp; i < rg.used; i += GROUPS) {
+      const uint64_t p = at + (uint64_t)i * R;
+      const float2v ml = *reinterpret_cast<const float2v*>(part_ml + p * 2);
+      const float keep = ml[0] == top ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - top);
+      sum += *reinterpret_cast<const float4v*>(part + p * D + x * 4) * keep;
+      below += ml[1] * keep;
+    }
+    lds[grp][x] = sum;
+    if (x == 0) lds_l[grp] = below;
+  }
+  __syncthreads();
+  if (grp == 0) {
+    for (int i = 1; i < GROUPS; ++i) {
+      sum += lds[i][x];
+      below += lds_l[i];
+    }
+    const uint32_t token = (r0 + r) / G, qh = head * G + (r0 + r) % G;
+    const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * (1.0f / below);
+    const uint2v out = {pack2(bf16, o[0], o[1]), pack2(bf16, o[2], o[3])};
+    *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + x * 4) = out;
+  }
+}
+
+constexpr int kWaves = 4;
+
+struct Plan {
+  UnitMap map;
+  uint32_t units, nc, splits;
+};
+
+Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
+  Plan p;
+  const uint32_t G = q_heads / c.heads;
+  const uint64_t mean = ((uint64_t)s.rows * G + s.seqs - 1) / s.seqs;  // packed rows of a sequence and head
+  p.nc = mean <= 16 || c.dim > 192 ? 1 : mean <= 32 || c.dim > 96 ? 2 : 4;
+  const uint32_t R = 16 * p.nc;
+  p.map = s.cu ? UnitMap{G, R, 1} : UnitMap{0, 1, (G + R - 1) / R};
+  p.units = (uint32_t)unit_count(p.map, s.rows, s.seqs);
+  uint64_t longest = (uint64_t)s.width << c.page_log;
+  if (window && window + 64 < longest) longest = window + 64;
+  const uint64_t most = (longest + kStep * kWaves - 1) / (kStep * kWaves);
+  const uint64_t base = (uint64_t)p.units * c.heads;
+  uint64_t want = (2048 + base - 1) / base;
+  p.splits = (uint32_t)(want < most ? want : most);
+  if (p.splits < 1) p.splits = 1;
+  return p;
+}
+
+template <bool E4M3, int D>
+hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
+                       hipStream_t st) {
+  const dim3 grid(p.units * p.splits, c.heads);
+  constexpr int T = 64 * kWaves;
+  if (p.nc == 1) k_attend_rows<E4M3, D, 1, kWaves><<<grid, T, 0, st>>>(c, s, p.map, a, bf16, p.splits);
+  else if constexpr (D <= 192) {
+    if (p.nc == 2) k_attend_rows<E4M3, D, 2, kWaves><<<grid, T, 0, st>>>(c, s, p.map, a, bf16, p.splits);
+    else if constexpr (D <= 96) k_attend_rows<E4M3, D, 4, kWaves><<<grid, T, 0, st>>>(c, s, p.map, a, bf16, p.splits);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const uint32_t R = 16 * p.nc;
+  k_attend_join<D><<<dim3(p.units * R, c.heads), 256, 0, st>>>(c, s, p.map, a, bf16, p.splits, R, p.units, kWaves);
+  return hipGetLastError();
+}
+
+template <bool E4M3>
+hipError_t launch_dim(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, hipStream_t st) {
+  const Plan p = plan_rows(c, s, a.q_heads, a.window);
+  switch (c.dim) {
+    case 64: return launch_rows<E4M3, 64>(c, s, bf16, a, p, st);
+    case 96: return launch_rows<E4M3, 96>(c, s, bf16, a, p, st);
+    case 128: return launch_rows<E4M3, 128>(c, s, bf16, a, p, st);
+    case 192: return launch_rows<E4M3, 192>(c, s, bf16, a, p, st);
+    case 256: return launch_rows<E4M3, 256>(c, s, bf16, a, p, st);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-uint64_t cache_attend_workspace(const CacheView&, const SeqView&, uint32_t, uint32_t) { return 0; }
+uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
+  if (!s.rows) return 0;
+  const Plan p = plan_rows(c, s, q_heads, window);
+  return p.splits == 1 ? 0 : (uint64_t)p.units * c.heads * p.splits * 16 * p.nc * (c.dim + 2) * sizeof(float);
+}
 
 hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, bool e4m3, int dtype, const AttendArgs& a,
                                hipStream_t st) {
-  const dim3 grid(s.rows, a.q_heads);
-  if (e4m3) {
-    if (dtype == LTC_BF16) k_cache_attend<true, LTC_BF16><<<grid, 64, 0, st>>>(c, s, a);
-    else k_cache_attend<true, LTC_FP16><<<grid, 64, 0, st>>>(c, s, a);
-  } else {
-    if (dtype == LTC_BF16) k_cache_attend<false, LTC_BF16><<<grid, 64, 0, st>>>(c, s, a);
-    else k_cache_attend<false, LTC_FP16><<<grid, 64, 0, st>>>(c, s, a);
-  }
-  return hipGetLastError();
+  const bool bf16 = dtype == LTC_BF16;
+  return e4m3 ? launch_dim<true>(c, s, bf16, a, st) : launch_dim<false>(c, s, bf16, a, st);
 }
 
 }  // namespace ltc
