@@ -14,12 +14,7 @@
 namespace ltc {
 namespace {
 
-typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef float float4v __attribute__((ext_vector_type(4)));
-typedef float float2v __attribute__((ext_vector_type(2)));
-typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
-typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 // A tile whose largest x + w is within 2^kSlack of the running bound keeps the
@@ -59,13 +54,6 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
   return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// Of the bytes at positions t..t+3, those in [lo, hi) as 0xff.
-__device__ __forceinline__ uint32_t byte_mask(int t, int lo, int hi) {
-  const int a = min(max(lo - t, 0), 4), b = min(max(hi - t, 0), 4);
-  const uint32_t below_b = (uint32_t)((1ull << (8 * b)) - 1), below_a = (uint32_t)((1ull << (8 * a)) - 1);
-  return below_b & ~below_a;
-}
-
 // The positions that a tile of packed rows looks at, in steps of kStep, and
 // how they are shared out: split i takes steps [i * per, (i + 1) * per).
 constexpr int kStep = 64;
@@ -95,10 +83,7 @@ __device__ __forceinline__ uint64_t partial_at(uint32_t unit, uint32_t heads, ui
   return ((((uint64_t)unit * heads + head) * splits) + split) * rows;
 }
 
-template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return (uint32_t)narrow<DT>(a) | (uint32_t)narrow<DT>(b) << 16;
-}
-__device__ __forceinline__ uint32_t pack2(bool bf16, float a, float b) {
+__device__ __forceinline__ uint32_t pack2_as(bool bf16, float a, float b) {
   return bf16 ? pack2<LTC_BF16>(a, b) : pack2<LTC_FP16>(a, b);
 }
 
@@ -414,7 +399,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
         const uint32_t token = (r0 + r) / G, qh = head * G + (r0 + r) % G;
         const float inv = below == 0.0f ? 0.0f : 1.0f / below;
         const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * inv;
-        uint2v packed16 = {pack2(bf16, o[0], o[1]), pack2(bf16, o[2], o[3])};
+        uint2v packed16 = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
         *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = packed16;
       }
     }
@@ -469,7 +454,7 @@ __global__ __launch_bounds__(256) void k_attend_join(CacheView c, SeqView s, Uni
     }
     const uint32_t token = (r0 + r) / G, qh = head * G + (r0 + r) % G;
     const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * (1.0f / below);
-    const uint2v out = {pack2(bf16, o[0], o[1]), pack2(bf16, o[2], o[3])};
+    const uint2v out = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
     *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + x * 4) = out;
   }
 }
