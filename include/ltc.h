@@ -530,7 +530,11 @@ int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k
  * heads).  d_out [rows][q_heads][dim] (16-byte aligned) gets
  * softmax(scale * q k^T) v, zeros for a row that sees nothing.  The workspace
  * has ltc_cache_attend_workspace_size() bytes, 256-byte aligned (none may be
- * needed, then d_ws may be NULL); its contents do not matter. */
+ * needed, then d_ws may be NULL).  Its first LTC_CACHE_WS_ZEROS bytes must be
+ * zero before the first call that uses it, and every call leaves them zero: a
+ * caller clears a workspace once and keeps it.  Calls that may run at the same
+ * time need workspaces of their own. */
+enum { LTC_CACHE_WS_ZEROS = 65536 };
 uint64_t ltc_cache_attend_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,
                                          uint32_t window);
 int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,

@@ -76,11 +76,28 @@ __device__ __forceinline__ Range range_of(const Span& sp, uint32_t tok0, uint32_
   return r;
 }
 
-// partial results of a split: [unit][head][split][row of the tile] numerators
-// (dim floats), then bound and sum (2 floats) in an array behind them
-__device__ __forceinline__ uint64_t partial_at(uint32_t unit, uint32_t heads, uint32_t head, uint32_t splits,
-                                               uint32_t split, uint32_t rows) {
-  return ((((uint64_t)unit * heads + head) * splits) + split) * rows;
+// The workspace: kCounters counters, all zero between calls, then the splits'
+// partial results: [unit][head][split][row of the tile] numerators (dim
+// floats), and bound and sum (2 floats) in an array behind them.
+constexpr uint32_t kCounters = 16384;
+constexpr uint64_t kCounterBytes = kCounters * 4;
+
+// Partial results travel between workgroups of any chiplet through atomic
+// accesses of the device's scope, which go past the chiplet's own L2.  The
+// writer's are waited for (wait_stores) before its counter is raised, so no
+// fence has to write an L2 back: with __threadfence() in every workgroup the
+// call of 64 rows at 1,000-6,000 positions took 462 us instead of 115.
+__device__ __forceinline__ void put2(float* p, float a, float b) {
+  const float2v x = {a, b};
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, x), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2v get2(const float* p) {
+  return __builtin_bit_cast(float2v, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                                       __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ __forceinline__ void wait_stores() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t pack2_as(bool bf16, float a, float b) {
@@ -112,6 +129,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
   constexpr int R = 16 * NC, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
   __shared__ float lds_acc[W][16][D + 4];
   __shared__ float lds_m[W][R], lds_l[W][R];
+  __shared__ bool lds_last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
   const uint32_t unit = blockIdx.x / splits, split = blockIdx.x % splits, head = blockIdx.y;
   const uint32_t G = a.q_heads / c.heads;
@@ -358,6 +376,12 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     if (next < step_end) load_v(v_off);
   }
 
+  auto store_row = [&](int r, int d, float4v sum, float below) {
+    const uint32_t token = (r0 + r) / G, qh = head * G + (r0 + r) % G;
+    const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * (1.0f / below);
+    const uint2v out = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
+    *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = out;
+  };
   // ---- the waves' parts together
   for (int nc = 0; nc < NC; ++nc) {
     l[nc] += __shfl_xor(l[nc], 16);
@@ -368,10 +392,10 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     }
   }
   __syncthreads();
-  float* part = static_cast<float*>(a.ws);
-  const uint64_t units = (uint64_t)gridDim.x / splits;
-  float* part_ml = part + units * c.heads * splits * R * D;
-  const uint64_t at = partial_at(unit, c.heads, head, splits, split, R);
+  const uint64_t tiles = (uint64_t)gridDim.x / splits * c.heads, tile = (uint64_t)unit * c.heads + head;
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounterBytes);
+  float* part_ml = part + tiles * splits * R * D;
+  const uint64_t at = (tile * splits + split) * R;
   for (int nc = 0; nc < NC; ++nc) {
     {
       const int r = nc * 16 + n;
@@ -392,70 +416,71 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
       for (int v = 0; v < W; ++v) top = fmaxf(top, lds_m[v][r]);
       for (int v = 0; v < W; ++v)
         below += lds_l[v][r] * (lds_m[v][r] == top ? 1.0f : __builtin_amdgcn_exp2f(lds_m[v][r] - top));
+      if (r0 + r >= packed) continue;
       if (rg.used > 1) {
-        *reinterpret_cast<float4v*>(part + (at + r) * D + d) = sum;
-        if (d == 0) *reinterpret_cast<float2v*>(part_ml + (at + r) * 2) = float2v{top, below};
-      } else if (r0 + r < packed) {
-        const uint32_t token = (r0 + r) / G, qh = head * G + (r0 + r) % G;
-        const float inv = below == 0.0f ? 0.0f : 1.0f / below;
-        const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * inv;
-        uint2v packed16 = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
-        *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = packed16;
+        put2(part + (at + r) * D + d, sum[0], sum[1]);
+        put2(part + (at + r) * D + d + 2, sum[2], sum[3]);
+        if (d == 0) put2(part_ml + (at + r) * 2, top, below);
+      } else {
+        store_row(r, d, sum, below);
       }
     }
     __syncthreads();
   }
-}
-
-// Joins the splits of a row, in their order: one workgroup of 256 for a
-// packed row of a tile, D / 4 lanes for its dims, the rest of them for every
-// 1024 / D-th split.
-template <int D>
-__global__ __launch_bounds__(256) void k_attend_join(CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16,
-                                                     uint32_t splits, uint32_t R, uint32_t units, int least) {
-  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
-  __shared__ float4v lds[GROUPS][LANES];
-  __shared__ float lds_l[GROUPS];
-  const uint32_t unit = blockIdx.x / R, r = blockIdx.x % R, head = blockIdx.y, G = a.q_heads / c.heads;
-  uint32_t seq;
-  Span sp;
-  uint64_t own;
-  const bool mine = locate_unit(c, s, map, unit, WaveCount{s, map, unit}, &seq, &sp, &own);
-  const uint32_t packed = sp.n * G;
-  if (!mine || !sp.ok || c.pages == 0 || own * R + r >= packed) return;
-  const uint32_t r0 = (uint32_t)own * R, r1 = min(r0 + R, packed);
-  const Range rg = range_of(sp, r0 / G, (r1 - 1) / G + 1, a.window, splits, least);
   if (rg.used <= 1) return;
-  const float* part = static_cast<const float*>(a.ws);
-  const float* part_ml = part + (uint64_t)units * c.heads * splits * R * D;
-  const uint64_t at = partial_at(unit, c.heads, head, splits, 0, R) + r;
-  float top = -INFINITY;
-  for (int i = threadIdx.x & 63; i < rg.used; i += 64) top = fmaxf(top, part_ml[(at + (uint64_t)i * R) * 2]);
-  for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+
+  // ---- the splits' parts together, by the workgroup that comes last (and in
+  // the splits' order, so that the order of coming does not matter).  One
+  // launch, where a second kernel would cost its launch: for one row at 777
+  // positions 12.8 us a call with it.
+  wait_stores();
+  __syncthreads();
+  if (threadIdx.x == 0) lds_last = atomicInc(static_cast<uint32_t*>(a.ws) + tile, (uint32_t)rg.used - 1) + 1 == (uint32_t)rg.used;
+  __syncthreads();
+  if (!lds_last) return;
+  constexpr int LANES = D / 4, GROUPS = 64 * W / LANES;
   const int grp = threadIdx.x / LANES, x = threadIdx.x % LANES;
-  float4v sum = {0, 0, 0, 0};
-  float below = 0.0f;
-  if (grp < GROUPS) {
-    for (int i = grp; i < rg.used; i += GROUPS) {
-      const uint64_t p = at + (uint64_t)i * R;
-      const float2v ml = *reinterpret_cast<const float2v*>(part_ml + p * 2);
-      const float keep = ml[0] == top ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - top);
-      sum += *reinterpret_cast<const float4v*>(part + p * D + x * 4) * keep;
-      below += ml[1] * keep;
-    }
-    lds[grp][x] = sum;
-    if (x == 0) lds_l[grp] = below;
+  const uint64_t at0 = tile * splits * R;
+  const int live = (int)min(packed - r0, (uint32_t)R);
+  // the rows' bounds, then their weighted sums: a group of lanes takes a row
+  // whole where there are rows for all groups, else every GROUPS-th split
+  for (int r = wave; r < live; r += W) {
+    float top = -INFINITY;
+    for (int i = lane; i < rg.used; i += 64) top = fmaxf(top, get2(part_ml + (at0 + (uint64_t)i * R + r) * 2)[0]);
+    for (int v = 32; v; v >>= 1) top = fmaxf(top, __shfl_xor(top, v));
+    if (lane == 0) lds_m[0][r] = top;
   }
   __syncthreads();
-  if (grp == 0) {
-    for (int i = 1; i < GROUPS; ++i) {
-      sum += lds[i][x];
-      below += lds_l[i];
+  auto gather = [&](int r, int i0, int di, float4v& sum, float& below) {
+    const float top = lds_m[0][r];
+#pragma unroll 4
+    for (int i = i0; i < rg.used; i += di) {
+      const uint64_t p = at0 + (uint64_t)i * R + r;
+      const float2v ml = get2(part_ml + p * 2);
+      const float keep = ml[0] == top ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - top);
+      const float2v lo = get2(part + p * D + x * 4), hi = get2(part + p * D + x * 4 + 2);
+      sum += float4v{lo[0], lo[1], hi[0], hi[1]} * keep;
+      below += ml[1] * keep;
     }
-    const uint32_t token = (r0 + r) / G, qh = head * G + (r0 + r) % G;
-    const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * (1.0f / below);
-    const uint2v out = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
-    *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + x * 4) = out;
+  };
+  float* lds_flat = &lds_acc[0][0][0];
+  for (int r = 0; r < live; ++r) {
+    float4v sum = {0, 0, 0, 0};
+    float below = 0.0f;
+    if (grp < GROUPS) {
+      gather(r, grp, GROUPS, sum, below);
+      *reinterpret_cast<float4v*>(lds_flat + (grp * LANES + x) * 4) = sum;
+      if (x == 0) lds_l[0][grp] = below;
+    }
+    __syncthreads();
+    if (grp == 0) {
+      for (int i = 1; i < GROUPS; ++i) {
+        sum += *reinterpret_cast<const float4v*>(lds_flat + (i * LANES + x) * 4);
+        below += lds_l[0][i];
+      }
+      store_row(r, x * 4, sum, below);
+    }
+    __syncthreads();
   }
 }
 
@@ -478,9 +503,9 @@ Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t 
   if (window && window + 64 < longest) longest = window + 64;
   const uint64_t most = (longest + kStep * kWaves - 1) / (kStep * kWaves);
   const uint64_t base = (uint64_t)p.units * c.heads;
-  uint64_t want = (2048 + base - 1) / base;
+  uint64_t want = (1024 + base - 1) / base;
   p.splits = (uint32_t)(want < most ? want : most);
-  if (p.splits < 1) p.splits = 1;
+  if (p.splits < 1 || base > kCounters) p.splits = 1;
   return p;
 }
 
@@ -494,10 +519,6 @@ hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const At
     if (p.nc == 2) k_attend_rows<E4M3, D, 2, kWaves><<<grid, T, 0, st>>>(c, s, p.map, a, bf16, p.splits);
     else if constexpr (D <= 96) k_attend_rows<E4M3, D, 4, kWaves><<<grid, T, 0, st>>>(c, s, p.map, a, bf16, p.splits);
   }
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
-  const uint32_t R = 16 * p.nc;
-  k_attend_join<D><<<dim3(p.units * R, c.heads), 256, 0, st>>>(c, s, p.map, a, bf16, p.splits, R, p.units, kWaves);
   return hipGetLastError();
 }
 
@@ -519,7 +540,7 @@ hipError_t launch_dim(const CacheView& c, const SeqView& s, bool bf16, const Att
 uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
   if (!s.rows) return 0;
   const Plan p = plan_rows(c, s, q_heads, window);
-  return p.splits == 1 ? 0 : (uint64_t)p.units * c.heads * p.splits * 16 * p.nc * (c.dim + 2) * sizeof(float);
+  return p.splits == 1 ? 0 : kCounterBytes + (uint64_t)p.units * c.heads * p.splits * 16 * p.nc * (c.dim + 2) * sizeof(float);
 }
 
 hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, bool e4m3, int dtype, const AttendArgs& a,

@@ -9,8 +9,8 @@ and attended to in place.
 A binding over ltc_cache_write, ltc_cache_read and ltc_cache_attend of
 include/ltc.h, where the layouts, the rounding and what happens with bad
 tables are written down.  Calls run on the current stream, allocate nothing
-but their outputs and workspace, and never synchronise, so they can be
-captured in a graph.
+but their outputs and a workspace that the cache keeps for each stream, and
+never synchronise, so they can be captured in a graph.
 
 Rows cu[i]..cu[i+1] of a call belong to sequence i and stand for its last
 positions, lengths[i] - (cu[i+1] - cu[i]) to lengths[i] - 1; without cu each
@@ -30,6 +30,7 @@ CACHE_DTYPES = {torch.bfloat16: 1, torch.float16: 2}
 PAGES = (16, 32, 64, 128, 256)
 DIMS = (64, 96, 128, 192, 256)
 BAD_PAGE, BAD_SEQUENCE = 1, 2
+WS_ZEROS = 65536
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds a Stream object: 2.7 us a call
 _pack_seqs = struct.Struct("=QQQQIIII").pack      # ltc_cache_seqs
@@ -72,6 +73,7 @@ class KVCache:
                                    pages, heads, dim, page, CODES[codes], CACHE_DTYPES[dtype])
         self._ref = ctypes.byref(self._struct)
         self._index = self.device.index
+        self._workspaces = {}  # stream -> tensor, its first bytes zero between calls
 
     @staticmethod
     def _shape(k_codes, v_codes, scales):
@@ -113,6 +115,19 @@ class KVCache:
             what = [n for b, n in ((BAD_PAGE, "a table entry outside the cache"),
                                    (BAD_SEQUENCE, "lengths or cu that contradict each other")) if bits & b]
             raise LTCError(-5, " and ".join(what))
+
+    def _workspace(self, need, stream):
+        """Device pointer and size of a workspace for a call on the stream.
+        Each stream keeps one, since its calls run in order; a captured call
+        gets its own, which lives and is cleared with the graph."""
+        captured = torch._C._cuda_isCurrentStreamCapturing()
+        ws = None if captured else self._workspaces.get(stream)
+        if ws is None or ws.numel() < need:
+            ws = torch.empty(1 << (need - 1).bit_length(), dtype=torch.uint8, device=self.device)
+            ws[:WS_ZEROS].zero_()
+            if not captured:
+                self._workspaces[stream] = ws
+        return ws.data_ptr(), ws.numel()
 
     def _seqs(self, table, lengths, cu, rows):
         """ltc_cache_seqs as bytes; what can be seen without the GPU is checked."""
@@ -184,9 +199,9 @@ def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None):
     rows, q_heads, dim = q.shape
     s = cache._seqs(table, lengths, cu, rows)
     out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
+    stream = _raw_stream(cache._index)
     need = cache._lib.ltc_cache_attend_workspace_size(cache._ref, s, q_heads, window)
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    ws, size = cache._workspace(need, stream) if need else (None, 0)
     _check(cache._lib.ltc_cache_attend(cache._ref, s, qr, q_heads, window, dim ** -0.5 if scale is None else scale,
-                                       out.data_ptr(), ws.data_ptr() if need else None, need,
-                                       _raw_stream(cache._index)), "cache_attend")
+                                       out.data_ptr(), ws, size, stream), "cache_attend")
     return out
