@@ -8,8 +8,11 @@ namespace {
 
 constexpr uint32_t kMaxPages = 1u << 30;   // table entries are 32-bit
 constexpr uint32_t kMaxHeads = 65535;      // a grid's second dimension
-constexpr uint32_t kMaxRows = 1u << 24;    // grid limit: workgroups * 256 work-items stay below 2^32
-constexpr uint32_t kMaxSeqs = 1u << 22;
+// grid limits: lanes of a grid's first dimension stay below 2^32, and the
+// workgroups of an attention are counted in 32 bits
+constexpr uint32_t kMaxRows = 1u << 24;
+constexpr uint32_t kMaxSeqs = 1u << 20;
+constexpr uint64_t kMaxAttend = 1ull << 31;  // (rows + sequences) * query heads
 
 bool aligned(const void* p, uintptr_t to) { return p && reinterpret_cast<uintptr_t>(p) % to == 0; }
 
@@ -63,6 +66,11 @@ int check_rows(const ltc_cache_rows* r, RowsView* out) {
   return LTC_OK;
 }
 
+int check_heads(const CacheView& c, const SeqView& s, uint32_t q_heads) {
+  if (!q_heads || q_heads % c.heads || q_heads > kMaxHeads) return LTC_ERR_INVALID_ARGUMENT;
+  return ((uint64_t)s.rows + s.seqs) * q_heads > kMaxAttend ? LTC_ERR_INVALID_ARGUMENT : LTC_OK;
+}
+
 int launched(hipError_t e) { return e == hipSuccess ? LTC_OK : LTC_ERR_HIP; }
 
 }  // namespace
@@ -101,7 +109,7 @@ uint64_t ltc_cache_attend_workspace_size(const ltc_cache* cache, const ltc_cache
                                          uint32_t window) {
   CacheView c;
   SeqView s;
-  if (check_cache(cache, &c) || check_seqs(seqs, &s) || !q_heads || q_heads % c.heads) return 0;
+  if (check_cache(cache, &c) || check_seqs(seqs, &s) || check_heads(c, s, q_heads)) return 0;
   return cache_attend_workspace(c, s, q_heads, window);
 }
 
@@ -113,7 +121,8 @@ int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const l
   int rc = check_cache(cache, &c);
   if (!rc) rc = check_seqs(seqs, &s);
   if (rc) return rc;
-  if (!q_heads || q_heads % c.heads || q_heads > kMaxHeads) return LTC_ERR_INVALID_ARGUMENT;
+  rc = check_heads(c, s, q_heads);
+  if (rc) return rc;
   if (window > 0x7fffffffu || !(scale > 0.0f && scale < 1e30f)) return LTC_ERR_INVALID_ARGUMENT;
   if (!s.rows) return LTC_OK;
   rc = check_rows(q, &a.q);

@@ -104,6 +104,27 @@ __device__ __forceinline__ uint32_t pack2_as(bool bf16, float a, float b) {
   return bf16 ? pack2<LTC_BF16>(a, b) : pack2<LTC_FP16>(a, b);
 }
 
+// Which head, unit and split a workgroup takes.  Workgroups go to the eight
+// chiplets in turn, and a chiplet's L2 holds what its workgroups read: so the
+// heads are shared out over the chiplets, as far as a power of two divides
+// them, and chiplets that have heads in common take every share-th of their
+// units.  The last units come first: a long prompt's last rows see the most.
+// share divides per_head, the units times splits of a head and a few numbers
+// without work.
+__host__ __device__ constexpr uint32_t chiplet_share(uint32_t heads) {
+  return heads % 8 == 0 ? 1 : heads % 4 == 0 ? 2 : heads % 2 == 0 ? 4 : 8;
+}
+__device__ __forceinline__ void place(uint32_t heads, uint32_t splits, uint32_t per_head, uint32_t* head,
+                                      uint32_t* unit, uint32_t* split) {
+  const uint32_t id = blockIdx.x + gridDim.x * blockIdx.y;
+  const uint32_t share = chiplet_share(heads), classes = 8 / share;
+  const uint32_t chiplet = id % 8, i = id / 8 * share + chiplet / classes;
+  *head = chiplet % classes + i / per_head * classes;
+  const uint32_t x = per_head - 1 - i % per_head;
+  *unit = x / splits;
+  *split = x % splits;
+}
+
 // waves for each SIMD that the kernel's registers are to leave room for
 constexpr int rows_occupancy(int D, int NC) { return D * NC <= 128 ? 3 : D * NC <= 256 && D < 256 ? 2 : 1; }
 
@@ -125,13 +146,16 @@ constexpr int rows_occupancy(int D, int NC) { return D * NC <= 128 ? 3 : D * NC 
 // flight for each wave.
 template <bool E4M3, int D, int NC, int W>
 __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16,
-                                                         uint32_t splits) {
+                                                                              uint32_t units, uint32_t splits,
+                                                                              uint32_t per_head) {
   constexpr int R = 16 * NC, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
   __shared__ float lds_acc[W][16][D + 4];
   __shared__ float lds_m[W][R], lds_l[W][R];
   __shared__ bool lds_last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const uint32_t unit = blockIdx.x / splits, split = blockIdx.x % splits, head = blockIdx.y;
+  uint32_t head, unit, split;
+  place(c.heads, splits, per_head, &head, &unit, &split);
+  if (head >= c.heads || unit >= units) return;
   const uint32_t G = a.q_heads / c.heads;
   uint32_t seq;
   Span sp;
@@ -150,7 +174,8 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
 
   // queries: lane (n, g) holds row n's dims of k-group g
   half8 q[NC][KS];
-  float factor[NC];
+  const float base = a.scale * kLog2e;
+  int up[NC];  // q holds the queries times 2^up
   int row_lo[NC], row_hi[NC];
   for (int nc = 0; nc < NC; ++nc) {
     const uint32_t r = r0 + nc * 16 + n;
@@ -164,7 +189,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
       const int d = x < 2 * KL ? (4 * (x / 2) + g) * 16 + (x & 1) * 8 : 64 * KL + g * 8;
       raw[x] = live ? *reinterpret_cast<const uint4v*>(src + d) : uint4v{0, 0, 0, 0};
     }
-    factor[nc] = a.scale * kLog2e;
+    up[nc] = 0;
     if (bf16) {
       // to fp16 by a power of two that brings the row's largest number to
       // 2^14..2^15: what is lost is below 2^-39 of it, less than the sum's
@@ -175,9 +200,8 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
       top = max(top, (uint32_t)__shfl_xor((int)top, 16));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32));
       const int e = (int)(top >> 7);  // biased exponent; 255: infinities or NaN, which no factor helps
-      const int up = e == 255 ? 0 : min(141 - e, 127);
-      factor[nc] *= power_of_two(-up);
-      const float f = power_of_two(up);
+      up[nc] = e == 255 ? 0 : min(141 - e, 126);
+      const float f = power_of_two(up[nc]);
       for (int x = 0; x < KS; ++x)
         for (int i = 0; i < 4; ++i) {
           q[nc][x][2 * i] = (_Float16)(widen<LTC_BF16>(raw[x][i] & 0xffffu) * f);
@@ -273,13 +297,13 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     const bool lost = tv < rg.hi && tv + 16 > rg.lo && !have_v;
     if (lost && n == 0) report(c, kCacheBadPage);
     const bool edge = t0 < all_lo || t0 + kStep > all_hi || __any(lost);
-    const float ks = power_of_two((int)(sc & 0xff) - 127);
+    const int ke = (int)(sc & 0xff) - 127;
     const int we = (int)(sc >> 8) - 127;
     const float w = (float)we;
     half8 p[NC][2];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      const float f = factor[nc] * ks;
+      const float f = __builtin_amdgcn_ldexpf(base, ke - up[nc]);
       if (edge) {
         for (int b = 0; b < 4; ++b)
           for (int i = 0; i < 4; ++i) {
@@ -392,7 +416,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     }
   }
   __syncthreads();
-  const uint64_t tiles = (uint64_t)gridDim.x / splits * c.heads, tile = (uint64_t)unit * c.heads + head;
+  const uint64_t tiles = (uint64_t)units * c.heads, tile = (uint64_t)unit * c.heads + head;
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounterBytes);
   float* part_ml = part + tiles * splits * R * D;
   const uint64_t at = (tile * splits + split) * R;
@@ -442,8 +466,9 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
   const int grp = threadIdx.x / LANES, x = threadIdx.x % LANES;
   const uint64_t at0 = tile * splits * R;
   const int live = (int)min(packed - r0, (uint32_t)R);
-  // the rows' bounds, then their weighted sums: a group of lanes takes a row
-  // whole where there are rows for all groups, else every GROUPS-th split
+  // the rows' bounds, then their weighted sums: a group of lanes takes rows
+  // whole, or, where there are fewer rows than groups, a row's every
+  // parts-th split
   for (int r = wave; r < live; r += W) {
     float top = -INFINITY;
     for (int i = lane; i < rg.used; i += 64) top = fmaxf(top, get2(part_ml + (at0 + (uint64_t)i * R + r) * 2)[0]);
@@ -451,10 +476,14 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     if (lane == 0) lds_m[0][r] = top;
   }
   __syncthreads();
-  auto gather = [&](int r, int i0, int di, float4v& sum, float& below) {
+  const int parts = max(GROUPS / live, 1), mine_of = grp % parts;
+  float* lds_flat = &lds_acc[0][0][0];
+  for (int r = grp / parts; r < live && grp < GROUPS; r += GROUPS / parts) {  // once, if parts > 1
     const float top = lds_m[0][r];
+    float4v sum = {0, 0, 0, 0};
+    float below = 0.0f;
 #pragma unroll 4
-    for (int i = i0; i < rg.used; i += di) {
+    for (int i = mine_of; i < rg.used; i += parts) {
       const uint64_t p = at0 + (uint64_t)i * R + r;
       const float2v ml = get2(part_ml + p * 2);
       const float keep = ml[0] == top ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - top);
@@ -462,33 +491,33 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
       sum += float4v{lo[0], lo[1], hi[0], hi[1]} * keep;
       below += ml[1] * keep;
     }
-  };
-  float* lds_flat = &lds_acc[0][0][0];
-  for (int r = 0; r < live; ++r) {
-    float4v sum = {0, 0, 0, 0};
-    float below = 0.0f;
-    if (grp < GROUPS) {
-      gather(r, grp, GROUPS, sum, below);
+    if (parts == 1) {
+      store_row(r, x * 4, sum, below);
+    } else {
       *reinterpret_cast<float4v*>(lds_flat + (grp * LANES + x) * 4) = sum;
       if (x == 0) lds_l[0][grp] = below;
     }
-    __syncthreads();
-    if (grp == 0) {
-      for (int i = 1; i < GROUPS; ++i) {
-        sum += *reinterpret_cast<const float4v*>(lds_flat + (i * LANES + x) * 4);
-        below += lds_l[0][i];
-      }
-      store_row(r, x * 4, sum, below);
-    }
-    __syncthreads();
   }
+  if (parts == 1) return;
+  __syncthreads();
+  if (mine_of != 0 || grp / parts >= live || grp >= GROUPS) return;
+  float4v sum = {0, 0, 0, 0};
+  float below = 0.0f;
+  for (int i = 0; i < parts; ++i) {
+    sum += *reinterpret_cast<const float4v*>(lds_flat + ((grp + i) * LANES + x) * 4);
+    below += lds_l[0][grp + i];
+  }
+  store_row(grp / parts, x * 4, sum, below);
 }
 
 constexpr int kWaves = 4;
+constexpr uint32_t kGridWidth = 1u << 20;  // times a workgroup's lanes below 2^32
 
 struct Plan {
   UnitMap map;
   uint32_t units, nc, splits;
+  uint32_t per_head;  // workgroups of a head
+  dim3 grid;
 };
 
 Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
@@ -506,18 +535,21 @@ Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t 
   uint64_t want = (1024 + base - 1) / base;
   p.splits = (uint32_t)(want < most ? want : most);
   if (p.splits < 1 || base > kCounters) p.splits = 1;
+  const uint32_t share = chiplet_share(c.heads);
+  p.per_head = (p.units * p.splits + share - 1) / share * share;
+  const uint64_t groups = (uint64_t)p.per_head * c.heads;  // a multiple of 8
+  p.grid = dim3((uint32_t)(groups < kGridWidth ? groups : kGridWidth), (uint32_t)((groups + kGridWidth - 1) / kGridWidth));
   return p;
 }
 
 template <bool E4M3, int D>
 hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
                        hipStream_t st) {
-  const dim3 grid(p.units * p.splits, c.heads);
   constexpr int T = 64 * kWaves;
-  if (p.nc == 1) k_attend_rows<E4M3, D, 1, kWaves><<<grid, T, 0, st>>>(c, s, p.map, a, bf16, p.splits);
+  if (p.nc == 1) k_attend_rows<E4M3, D, 1, kWaves><<<p.grid, T, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
   else if constexpr (D <= 192) {
-    if (p.nc == 2) k_attend_rows<E4M3, D, 2, kWaves><<<grid, T, 0, st>>>(c, s, p.map, a, bf16, p.splits);
-    else if constexpr (D <= 96) k_attend_rows<E4M3, D, 4, kWaves><<<grid, T, 0, st>>>(c, s, p.map, a, bf16, p.splits);
+    if (p.nc == 2) k_attend_rows<E4M3, D, 2, kWaves><<<p.grid, T, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
+    else if constexpr (D <= 96) k_attend_rows<E4M3, D, 4, kWaves><<<p.grid, T, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
   }
   return hipGetLastError();
 }
