@@ -229,10 +229,10 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
   const uint32_t page_mask = (1u << c.page_log) - 1;
   const int kb = n >> 2;  // the block whose tokens' keys this lane reads
   const int32_t* table = s.table + seq * s.table_stride;
-  // byte offset of the 16 tokens at t within k or v, and whether they have a page
-  auto block_at = [&](int t, bool* have) -> uint64_t {
-    const bool want = t < rg.hi;
-    const int32_t p = want ? table[(uint32_t)t >> c.page_log] : -1;
+  // the table's entry for the 16 tokens at t, -1 behind the end; and their
+  // byte offset within k or v, and whether they have a page
+  auto page_of = [&](int t) -> int32_t { return t < rg.hi ? table[(uint32_t)t >> c.page_log] : -1; };
+  auto block_at = [&](int t, int32_t p, bool* have) -> uint64_t {
     *have = (uint32_t)p < c.pages;
     return head_offset(c, *have ? (uint32_t)p : 0, head) + (((uint32_t)t & page_mask) >> 4) * (16 * D);
   };
@@ -253,19 +253,24 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     const uint8_t* p = c.v + off + n * 16;
     for (int i = 0; i < DB; ++i) vr[i] = *reinterpret_cast<const uint4v*>(p + i * 256);
   };
-  auto load_scales = [&](int t, bool have) -> uint32_t {
-    const int32_t p = have ? table[(uint32_t)t >> c.page_log] : 0;
-    return *reinterpret_cast<const uint16_t*>(c.scales + ((uint64_t)p * c.heads + head) * 2);
+  auto load_scales = [&](int32_t p, bool have) -> uint32_t {
+    return *reinterpret_cast<const uint16_t*>(c.scales + ((uint64_t)(have ? (uint32_t)p : 0) * c.heads + head) * 2);
   };
 
+  // table entries are read a step before the addresses that need them
   bool have_k;
   uint64_t v_off = 0;
+  int32_t k_page = -1, v_page = -1;
   if (step < step_end) {
-    const uint64_t k_off = block_at(step * kStep + kb * 16, &have_k);
-    v_off = block_at(step * kStep + g * 16, &next_have_v);
+    k_page = page_of(step * kStep + kb * 16);
+    v_page = page_of(step * kStep + g * 16);
+    const uint64_t k_off = block_at(step * kStep + kb * 16, k_page, &have_k);
+    v_off = block_at(step * kStep + g * 16, v_page, &next_have_v);
     load_k(k_off);
     load_v(v_off);
-    scales = load_scales(step * kStep + g * 16, next_have_v);
+    scales = load_scales(v_page, next_have_v);
+    k_page = page_of((step + W) * kStep + kb * 16);
+    v_page = page_of((step + W) * kStep + g * 16);
   }
   for (; step < step_end; step += W) {
     const int t0 = step * kStep, tv = t0 + g * 16;
@@ -288,10 +293,12 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     const int next = step + W;
     uint64_t next_v = v_off;
     if (next < step_end) {
-      const uint64_t k_off = block_at(next * kStep + kb * 16, &have_k);
-      next_v = block_at(next * kStep + g * 16, &next_have_v);
+      const uint64_t k_off = block_at(next * kStep + kb * 16, k_page, &have_k);
+      next_v = block_at(next * kStep + g * 16, v_page, &next_have_v);
       load_k(k_off);
-      scales = load_scales(next * kStep + g * 16, next_have_v);
+      scales = load_scales(v_page, next_have_v);
+      k_page = page_of((next + W) * kStep + kb * 16);
+      v_page = page_of((next + W) * kStep + g * 16);
     }
     // ---- weights
     const bool lost = tv < rg.hi && tv + 16 > rg.lo && !have_v;
@@ -303,23 +310,20 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     half8 p[NC][2];
 #pragma unroll
     for (int nc = 0; nc < NC; ++nc) {
-      const float f = __builtin_amdgcn_ldexpf(base, ke - up[nc]);
+      // not 0: hidden scores are -infinity
+      const float f = fmaxf(__builtin_amdgcn_ldexpf(base, ke - up[nc]), 0x1p-126f);
       if (edge) {
         for (int b = 0; b < 4; ++b)
           for (int i = 0; i < 4; ++i) {
             const int t = tv + 4 * b + i;
             const bool seen = t >= row_lo[nc] && t < row_hi[nc] && have_v;
-            // hidden: far below everything, but no infinity, so that no
-            // difference of infinities arises
-            st[nc][b][i] = seen ? fmaf(st[nc][b][i], f, w) : -INFINITY;
+            st[nc][b][i] = seen ? st[nc][b][i] : -INFINITY;
           }
-      } else {
-        for (int b = 0; b < 4; ++b)
-          for (int i = 0; i < 4; ++i) st[nc][b][i] = fmaf(st[nc][b][i], f, w);
       }
       float top = st[nc][0][0];
       for (int b = 0; b < 4; ++b)
         for (int i = 0; i < 4; ++i) top = fmaxf(top, st[nc][b][i]);
+      top = fmaf(top, f, w);
       if (__any(top > m[nc] + kSlack)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -329,11 +333,12 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
         l[nc] *= keep;
         for (int i = 0; i < DB; ++i) acc[nc][i] *= keep;
       }
-      const float bound = m[nc] == -INFINITY ? 0.0f : m[nc];  // nothing seen yet: every weight is 0
+      // nothing seen yet: every weight is 0
+      const float shift = m[nc] == -INFINITY ? 0.0f : w - m[nc];
       float sum = 0.0f;
       for (int b = 0; b < 4; ++b)
         for (int i = 0; i < 4; ++i) {
-          const float u = __builtin_amdgcn_exp2f(st[nc][b][i] - bound);
+          const float u = __builtin_amdgcn_exp2f(fmaf(st[nc][b][i], f, shift));
           sum += u;
           p[nc][b >> 1][(b & 1) * 4 + i] = (_Float16)u;
         }
@@ -462,7 +467,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
   if (threadIdx.x == 0) lds_last = atomicInc(static_cast<uint32_t*>(a.ws) + tile, (uint32_t)rg.used - 1) + 1 == (uint32_t)rg.used;
   __syncthreads();
   if (!lds_last) return;
-  constexpr int LANES = D / 4, GROUPS = 64 * W / LANES;
+  constexpr int LANES = D / 4, GROUPS = 64 * W / LANES, kAhead = 8;
   const int grp = threadIdx.x / LANES, x = threadIdx.x % LANES;
   const uint64_t at0 = tile * splits * R;
   const int live = (int)min(packed - r0, (uint32_t)R);
@@ -482,14 +487,24 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     const float top = lds_m[0][r];
     float4v sum = {0, 0, 0, 0};
     float below = 0.0f;
-#pragma unroll 4
-    for (int i = mine_of; i < rg.used; i += parts) {
-      const uint64_t p = at0 + (uint64_t)i * R + r;
-      const float2v ml = get2(part_ml + p * 2);
-      const float keep = ml[0] == top ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - top);
-      const float2v lo = get2(part + p * D + x * 4), hi = get2(part + p * D + x * 4 + 2);
-      sum += float4v{lo[0], lo[1], hi[0], hi[1]} * keep;
-      below += ml[1] * keep;
+    // kAhead splits' loads at once: they come from beyond the L2
+    for (int i0 = mine_of; i0 < rg.used; i0 += kAhead * parts) {
+      float2v ml[kAhead], lo[kAhead], hi[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const uint64_t p = at0 + (uint64_t)min(i0 + j * parts, rg.used - 1) * R + r;
+        ml[j] = get2(part_ml + p * 2);
+        lo[j] = get2(part + p * D + x * 4);
+        hi[j] = get2(part + p * D + x * 4 + 2);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        float keep = ml[j][0] == top ? 1.0f : __builtin_amdgcn_exp2f(ml[j][0] - top);
+        if (i0 + j * parts < rg.used) {
+          sum += float4v{lo[j][0], lo[j][1], hi[j][0], hi[j][1]} * keep;
+          below += ml[j][1] * keep;
+        }
+      }
     }
     if (parts == 1) {
       store_row(r, x * 4, sum, below);
@@ -511,6 +526,10 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
 }
 
 constexpr int kWaves = 4;
+// Workgroups that the splits are to make: two for each CU.  One row at 131,071
+// positions with 256 / 512 / 768 / 1024 of them: 64 / 61 / 67 / 75 us; 16
+// sequences of 5 rows: 39 / 33 / 41 / 43 us.  More read faster and join slower.
+constexpr uint32_t kFill = 512;
 constexpr uint32_t kGridWidth = 1u << 20;  // times a workgroup's lanes below 2^32
 
 struct Plan {
@@ -532,7 +551,7 @@ Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t 
   if (window && window + 64 < longest) longest = window + 64;
   const uint64_t most = (longest + kStep * kWaves - 1) / (kStep * kWaves);
   const uint64_t base = (uint64_t)p.units * c.heads;
-  uint64_t want = (1024 + base - 1) / base;
+  const uint64_t want = (kFill + base - 1) / base;
   p.splits = (uint32_t)(want < most ? want : most);
   if (p.splits < 1 || base > kCounters) p.splits = 1;
   const uint32_t share = chiplet_share(c.heads);
