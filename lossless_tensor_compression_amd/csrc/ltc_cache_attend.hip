@@ -125,6 +125,174 @@ __device__ __forceinline__ void place(uint32_t heads, uint32_t splits, uint32_t 
   *split = x % splits;
 }
 
+// A denominator's part from one bound to another.  Where pages' scales lie far
+// apart it may be large while 2^(from - to) is below fp32's numbers: so that
+// comes in two halves.
+__device__ __forceinline__ float rebase(float l, float from, float to) {
+  const float half = __builtin_amdgcn_exp2f(0.5f * (from - to));
+  return from == to ? l : l * half * half;
+}
+
+// What a wave keeps of its 16 * NC rows; lane 16 g + n has row n of each 16.
+template <int D, int NC> struct Rows {
+  half8 q[NC][D / 32];     // the k-group g of the queries, times 2^up
+  int up[NC];
+  int lo[NC], hi[NC];      // the positions [lo, hi) that the row sees
+  float4v acc[NC][D / 16]; // dims 16 i + 4 g + 0..3 of the numerator
+  float m[NC], l[NC];      // bound, and the lane's part of the denominator
+  uint64_t nan[NC];        // bit 4 i + j: acc[nc][i][j] met a NaN among the values
+};
+
+// Rows r0.. of a sequence and head; those from packed on are none, and see nothing.
+template <int D, int NC>
+__device__ __forceinline__ void load_rows(Rows<D, NC>& w, const AttendArgs& a, const Span& sp, uint32_t head, uint32_t G,
+                                          uint32_t r0, uint32_t packed, bool bf16, int n, int g) {
+  constexpr int KS = D / 32, KL = D / 64;
+  for (int nc = 0; nc < NC; ++nc) {
+    const uint32_t r = r0 + nc * 16 + n;
+    const bool live = r < packed;
+    const uint32_t token = live ? r / G : 0, qh = head * G + (live ? r % G : 0);
+    const uint16_t* src = a.q.base + (uint64_t)(sp.row0 + token) * a.q.row_stride + (uint64_t)qh * a.q.head_stride;
+    w.hi[nc] = live ? (int)(sp.start + token) + 1 : 0;
+    w.lo[nc] = a.window ? max(w.hi[nc] - (int)a.window, 0) : 0;
+    uint4v raw[KS];
+    for (int x = 0; x < KS; ++x) {
+      const int d = x < 2 * KL ? (4 * (x / 2) + g) * 16 + (x & 1) * 8 : 64 * KL + g * 8;
+      raw[x] = live ? *reinterpret_cast<const uint4v*>(src + d) : uint4v{0, 0, 0, 0};
+    }
+    w.up[nc] = 0;
+    if (bf16) {
+      // to fp16 by a power of two that brings the row's largest number to
+      // 2^14..2^15: what is lost is below 2^-39 of it, less than the sum's
+      // own rounding in fp32
+      uint32_t top = 0;
+      for (int x = 0; x < KS; ++x)
+        for (int i = 0; i < 4; ++i) top = max(top, max(raw[x][i] & 0x7fffu, (raw[x][i] >> 16) & 0x7fffu));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+      const int e = (int)(top >> 7);  // biased exponent; 255: infinities or NaN, which no factor helps
+      w.up[nc] = e == 255 ? 0 : min(141 - e, 126);
+      const float f = power_of_two(w.up[nc]);
+      for (int x = 0; x < KS; ++x)
+        for (int i = 0; i < 4; ++i) {
+          w.q[nc][x][2 * i] = (_Float16)(widen<LTC_BF16>(raw[x][i] & 0xffffu) * f);
+          w.q[nc][x][2 * i + 1] = (_Float16)(widen<LTC_BF16>(raw[x][i] >> 16) * f);
+        }
+    } else {
+      for (int x = 0; x < KS; ++x) w.q[nc][x] = __builtin_bit_cast(half8, raw[x]);
+    }
+    w.m[nc] = -INFINITY;
+    w.l[nc] = 0.0f;
+    w.nan[nc] = 0;
+    for (int i = 0; i < D / 16; ++i) w.acc[nc][i] = float4v{0, 0, 0, 0};
+  }
+}
+
+// The products of a step to weights: st[nc][b][i] is the one of the token at
+// tv + 4 b + i, sc the scales of the lane's 16 tokens.  edge: some row does not
+// see some token, or it has no page.
+template <int D, int NC>
+__device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], float base,
+                                             uint32_t sc, int tv, bool edge, bool have) {
+  const int ke = (int)(sc & 0xff) - 127, we = (int)(sc >> 8) - 127;
+  const float wv = (float)we;
+#pragma unroll
+  for (int nc = 0; nc < NC; ++nc) {
+    // not 0: hidden scores are -infinity
+    const float f = fmaxf(__builtin_amdgcn_ldexpf(base, ke - w.up[nc]), 0x1p-126f);
+    if (edge) {
+      for (int b = 0; b < 4; ++b)
+        for (int i = 0; i < 4; ++i) {
+          const int t = tv + 4 * b + i;
+          const bool seen = t >= w.lo[nc] && t < w.hi[nc] && have;
+          st[nc][b][i] = seen ? st[nc][b][i] : -INFINITY;
+        }
+    }
+    float top = st[nc][0][0];
+    for (int b = 0; b < 4; ++b)
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, st[nc][b][i]);
+    top = fmaf(top, f, wv);
+    if (__any(top > w.m[nc] + kSlack)) {
+      float now = fmaxf(top, __shfl_xor(top, 16));
+      now = fmaxf(now, __shfl_xor(now, 32));
+      now = fmaxf(now, w.m[nc]);
+      const float keep = now == w.m[nc] ? 1.0f : __builtin_amdgcn_exp2f(w.m[nc] - now);
+      w.l[nc] = rebase(w.l[nc], w.m[nc], now);
+      w.m[nc] = now;
+      for (int i = 0; i < D / 16; ++i) w.acc[nc][i] *= keep;
+    }
+    // weights near or below fp32's smallest are nothing above the fraction, but
+    // if their scale is as small they may be something below it
+    const bool tiny = top < w.m[nc] - 100.0f && top > -INFINITY;
+    float lift = 0.0f;
+    if (__any(tiny)) {
+      for (int b = 0; b < 4; ++b)
+        for (int i = 0; i < 4; ++i) lift += __builtin_amdgcn_exp2f(fmaf(st[nc][b][i], f, wv - top));
+      lift = rebase(lift, top, w.m[nc] + wv);
+    }
+    // nothing seen yet: every weight is 0
+    const float shift = w.m[nc] == -INFINITY ? 0.0f : wv - w.m[nc];
+    float sum = 0.0f;
+    for (int b = 0; b < 4; ++b)
+      for (int i = 0; i < 4; ++i) {
+        const float u = __builtin_amdgcn_exp2f(fmaf(st[nc][b][i], f, shift));
+        sum += u;
+        p[nc][b >> 1][(b & 1) * 4 + i] = (_Float16)u;
+      }
+    sum = __builtin_amdgcn_ldexpf(sum, -we);
+    w.l[nc] += tiny ? lift : sum;
+  }
+}
+
+// NaN among a step's value codes (the lane's 16 of dim 16 i + n are at
+// v + 256 i): the rows that see one take note of it, by a product of
+// indicators, so that the codes can lose it before they meet the weights of
+// rows that do not (0 * NaN is NaN).
+template <int D, int NC>
+__device__ __forceinline__ void note_nan(Rows<D, NC>& w, int tv, bool have, const uint8_t* v) {
+  asm volatile("" : "+v"(tv));  // nothing of this before the branch that leads here
+  for (int nc = 0; nc < NC; ++nc) {
+    half8 ind[2];
+    for (int b = 0; b < 4; ++b)
+      for (int i = 0; i < 4; ++i) {
+        const int t = tv + 4 * b + i;
+        ind[b >> 1][(b & 1) * 4 + i] = (_Float16)(t >= w.lo[nc] && t < w.hi[nc] && have ? 1.0f : 0.0f);
+      }
+#pragma unroll 1
+    for (int i = 0; i < D / 16; ++i) {  // a loop over memory: rare, and it must not cost registers
+      const uint4v x = *reinterpret_cast<const uint4v*>(v + i * 256);
+      float4v hit = {0, 0, 0, 0};
+      for (int h = 0; h < 2; ++h) {
+        half8 is;
+        for (int j = 0; j < 8; ++j)
+          is[j] = (_Float16)(nan_bytes(x[2 * h + j / 4]) >> (8 * (j & 3) + 7) & 1 ? 1.0f : 0.0f);
+        hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(is, ind[h], hit, 0, 0, 0);
+      }
+      for (int j = 0; j < 4; ++j) w.nan[nc] |= (uint64_t)(hit[j] > 0.0f) << (4 * i + j);
+    }
+  }
+}
+
+template <int D, int NC> __device__ __forceinline__ void apply_nan(Rows<D, NC>& w) {
+  for (int nc = 0; nc < NC; ++nc)
+    if (__any(w.nan[nc] != 0))
+      for (int i = 0; i < D / 16; ++i)
+        for (int j = 0; j < 4; ++j)
+          if (w.nan[nc] >> (4 * i + j) & 1) w.acc[nc][i][j] = __builtin_nanf("");
+}
+
+__device__ __forceinline__ uint32_t without_nan(uint32_t x) { return x & ~((nan_bytes(x) >> 7) * 0xffu); }
+
+// dims d..d+3 of row r of the sequence and head
+template <int D>
+__device__ __forceinline__ void store_row(const AttendArgs& a, const Span& sp, uint32_t head, uint32_t G, bool bf16,
+                                          uint32_t r, int d, float4v sum, float below) {
+  const uint32_t token = r / G, qh = head * G + r % G;
+  const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * (1.0f / below);
+  const uint2v out = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
+  *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = out;
+}
+
 // waves for each SIMD that the kernel's registers are to leave room for
 constexpr int rows_occupancy(int D, int NC) { return D * NC <= 128 ? 3 : D * NC <= 256 && D < 256 ? 2 : 1; }
 
@@ -145,9 +313,8 @@ constexpr int rows_occupancy(int D, int NC) { return D * NC <= 128 ? 3 : D * NC 
 // step's are used up, and so for values, so one step (2 * 64 * D bytes) is in
 // flight for each wave.
 template <bool E4M3, int D, int NC, int W>
-__global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16,
-                                                                              uint32_t units, uint32_t splits,
-                                                                              uint32_t per_head) {
+__global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
+    CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16, uint32_t units, uint32_t splits, uint32_t per_head) {
   constexpr int R = 16 * NC, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
   __shared__ float lds_acc[W][16][D + 4];
   __shared__ float lds_m[W][R], lds_l[W][R];
@@ -172,53 +339,9 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
   }
   if ((int)split >= max(rg.used, 1)) return;
 
-  // queries: lane (n, g) holds row n's dims of k-group g
-  half8 q[NC][KS];
   const float base = a.scale * kLog2e;
-  int up[NC];  // q holds the queries times 2^up
-  int row_lo[NC], row_hi[NC];
-  for (int nc = 0; nc < NC; ++nc) {
-    const uint32_t r = r0 + nc * 16 + n;
-    const bool live = r < packed;
-    const uint32_t token = live ? r / G : 0, qh = head * G + (live ? r % G : 0);
-    const uint16_t* src = a.q.base + (uint64_t)(sp.row0 + token) * a.q.row_stride + (uint64_t)qh * a.q.head_stride;
-    row_hi[nc] = live ? (int)(sp.start + token) + 1 : 0;
-    row_lo[nc] = a.window ? max(row_hi[nc] - (int)a.window, 0) : 0;
-    uint4v raw[KS];
-    for (int x = 0; x < KS; ++x) {
-      const int d = x < 2 * KL ? (4 * (x / 2) + g) * 16 + (x & 1) * 8 : 64 * KL + g * 8;
-      raw[x] = live ? *reinterpret_cast<const uint4v*>(src + d) : uint4v{0, 0, 0, 0};
-    }
-    up[nc] = 0;
-    if (bf16) {
-      // to fp16 by a power of two that brings the row's largest number to
-      // 2^14..2^15: what is lost is below 2^-39 of it, less than the sum's
-      // own rounding in fp32
-      uint32_t top = 0;
-      for (int x = 0; x < KS; ++x)
-        for (int i = 0; i < 4; ++i) top = max(top, max(raw[x][i] & 0x7fffu, (raw[x][i] >> 16) & 0x7fffu));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-      const int e = (int)(top >> 7);  // biased exponent; 255: infinities or NaN, which no factor helps
-      up[nc] = e == 255 ? 0 : min(141 - e, 126);
-      const float f = power_of_two(up[nc]);
-      for (int x = 0; x < KS; ++x)
-        for (int i = 0; i < 4; ++i) {
-          q[nc][x][2 * i] = (_Float16)(widen<LTC_BF16>(raw[x][i] & 0xffffu) * f);
-          q[nc][x][2 * i + 1] = (_Float16)(widen<LTC_BF16>(raw[x][i] >> 16) * f);
-        }
-    } else {
-      for (int x = 0; x < KS; ++x) q[nc][x] = __builtin_bit_cast(half8, raw[x]);
-    }
-  }
-
-  float4v acc[NC][DB];
-  float m[NC], l[NC];
-  for (int nc = 0; nc < NC; ++nc) {
-    m[nc] = -INFINITY;
-    l[nc] = 0.0f;
-    for (int i = 0; i < DB; ++i) acc[nc][i] = float4v{0, 0, 0, 0};
-  }
+  Rows<D, NC> w;
+  load_rows<D, NC>(w, a, sp, head, G, r0, packed, bf16, n, g);
   // positions that every row sees need no masks
   const int all_lo = a.window ? max((int)(sp.start + (r1 - 1) / G) + 1 - (int)a.window, 0) : 0;
   const int all_hi = (int)(sp.start + r0 / G) + 1;
@@ -288,7 +411,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
                                     : codes_to_half<E4M3>(kt[b][0], kt[b][1]);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
-          st[nc][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, q[nc][x], st[nc][b], 0, 0, 0);
+          st[nc][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w.q[nc][x], st[nc][b], 0, 0, 0);
       }
     const int next = step + W;
     uint64_t next_v = v_off;
@@ -304,46 +427,8 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     const bool lost = tv < rg.hi && tv + 16 > rg.lo && !have_v;
     if (lost && n == 0) report(c, kCacheBadPage);
     const bool edge = t0 < all_lo || t0 + kStep > all_hi || __any(lost);
-    const int ke = (int)(sc & 0xff) - 127;
-    const int we = (int)(sc >> 8) - 127;
-    const float w = (float)we;
     half8 p[NC][2];
-#pragma unroll
-    for (int nc = 0; nc < NC; ++nc) {
-      // not 0: hidden scores are -infinity
-      const float f = fmaxf(__builtin_amdgcn_ldexpf(base, ke - up[nc]), 0x1p-126f);
-      if (edge) {
-        for (int b = 0; b < 4; ++b)
-          for (int i = 0; i < 4; ++i) {
-            const int t = tv + 4 * b + i;
-            const bool seen = t >= row_lo[nc] && t < row_hi[nc] && have_v;
-            st[nc][b][i] = seen ? st[nc][b][i] : -INFINITY;
-          }
-      }
-      float top = st[nc][0][0];
-      for (int b = 0; b < 4; ++b)
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, st[nc][b][i]);
-      top = fmaf(top, f, w);
-      if (__any(top > m[nc] + kSlack)) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float now = fmaxf(m[nc], top);
-        const float keep = now == m[nc] ? 1.0f : __builtin_amdgcn_exp2f(m[nc] - now);
-        m[nc] = now;
-        l[nc] *= keep;
-        for (int i = 0; i < DB; ++i) acc[nc][i] *= keep;
-      }
-      // nothing seen yet: every weight is 0
-      const float shift = m[nc] == -INFINITY ? 0.0f : w - m[nc];
-      float sum = 0.0f;
-      for (int b = 0; b < 4; ++b)
-        for (int i = 0; i < 4; ++i) {
-          const float u = __builtin_amdgcn_exp2f(fmaf(st[nc][b][i], f, shift));
-          sum += u;
-          p[nc][b >> 1][(b & 1) * 4 + i] = (_Float16)u;
-        }
-      l[nc] += __builtin_amdgcn_ldexpf(sum, -we);
-    }
+    step_weights<D, NC>(w, st, p, base, sc, tv, edge, have_v);
     // ---- O^T
     if (edge) {
       // codes that no row sees may be anything, and 0 * NaN is NaN
@@ -352,42 +437,15 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
         for (int i = 0; i < DB; ++i) vr[i][dw] &= keep;
       }
       if constexpr (E4M3) {
-        // a NaN that some rows see and others do not: those that do get it
-        // from a product of indicators, and the codes lose it
         uint32_t any = 0;
         for (int i = 0; i < DB; ++i)
           for (int dw = 0; dw < 4; ++dw) any |= nan_bytes(vr[i][dw]);
         if (__any(any != 0)) {
-          for (int nc = 0; nc < NC; ++nc) {
-            half8 ind[2];
-            for (int b = 0; b < 4; ++b)
-              for (int i = 0; i < 4; ++i) {
-                const int t = tv + 4 * b + i;
-                ind[b >> 1][(b & 1) * 4 + i] = (_Float16)(t >= row_lo[nc] && t < row_hi[nc] && have_v ? 1.0f : 0.0f);
-              }
-            uint64_t hits = 0;
-#pragma unroll 1
-            for (int i = 0; i < DB; ++i) {  // a loop over memory: rare, and it must not cost registers
-              uint4v x = *reinterpret_cast<const uint4v*>(c.v + v_off + n * 16 + i * 256);
-              float4v hit = {0, 0, 0, 0};
-              for (int h = 0; h < 2; ++h) {
-                half8 is;
-                for (int j = 0; j < 8; ++j)
-                  is[j] = (_Float16)((nan_bytes(x[2 * h + j / 4]) >> (8 * (j & 3) + 7)) & 1 ? 1.0f : 0.0f);
-                hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(is, ind[h], hit, 0, 0, 0);
-              }
-              for (int j = 0; j < 4; ++j) hits |= (uint64_t)(hit[j] > 0.0f) << (4 * i + j);
-            }
-            for (int i = 0; i < DB; ++i)
-              for (int j = 0; j < 4; ++j)
-                if (hits >> (4 * i + j) & 1) acc[nc][i][j] = __builtin_nanf("");
-          }
+          note_nan<D, NC>(w, tv, have_v, c.v + v_off + n * 16);
           for (int dw = 0; dw < 4; ++dw) {
             const uint32_t keep = have_v ? byte_mask(tv + 4 * dw, rg.lo, rg.hi) : 0;
-            for (int i = 0; i < DB; ++i) {
-              const uint32_t x = *reinterpret_cast<const uint32_t*>(c.v + v_off + n * 16 + i * 256 + dw * 4) & keep;
-              vr[i][dw] = x & ~((nan_bytes(x) >> 7) * 0xffu);
-            }
+            for (int i = 0; i < DB; ++i)
+              vr[i][dw] = without_nan(*reinterpret_cast<const uint32_t*>(c.v + v_off + n * 16 + i * 256 + dw * 4) & keep);
           }
         }
       }
@@ -399,25 +457,20 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
         const half8 v8 = codes_to_half<E4M3>(vr[i][2 * h], vr[i][2 * h + 1]);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
-          acc[nc][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p[nc][h], acc[nc][i], 0, 0, 0);
+          w.acc[nc][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p[nc][h], w.acc[nc][i], 0, 0, 0);
       }
     v_off = next_v;
     if (next < step_end) load_v(v_off);
   }
 
-  auto store_row = [&](int r, int d, float4v sum, float below) {
-    const uint32_t token = (r0 + r) / G, qh = head * G + (r0 + r) % G;
-    const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * (1.0f / below);
-    const uint2v out = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
-    *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = out;
-  };
+  if constexpr (E4M3) apply_nan<D, NC>(w);
   // ---- the waves' parts together
   for (int nc = 0; nc < NC; ++nc) {
-    l[nc] += __shfl_xor(l[nc], 16);
-    l[nc] += __shfl_xor(l[nc], 32);
+    w.l[nc] += __shfl_xor(w.l[nc], 16);
+    w.l[nc] += __shfl_xor(w.l[nc], 32);
     if (g == 0) {
-      lds_m[wave][nc * 16 + n] = m[nc];
-      lds_l[wave][nc * 16 + n] = l[nc];
+      lds_m[wave][nc * 16 + n] = w.m[nc];
+      lds_l[wave][nc * 16 + n] = w.l[nc];
     }
   }
   __syncthreads();
@@ -430,9 +483,9 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
       const int r = nc * 16 + n;
       float top = -INFINITY;
       for (int v = 0; v < W; ++v) top = fmaxf(top, lds_m[v][r]);
-      const float keep = m[nc] == top ? 1.0f : __builtin_amdgcn_exp2f(m[nc] - top);
+      const float keep = w.m[nc] == top ? 1.0f : __builtin_amdgcn_exp2f(w.m[nc] - top);
       for (int i = 0; i < DB; ++i) {
-        const float4v x = acc[nc][i] * keep;
+        const float4v x = w.acc[nc][i] * keep;
         *reinterpret_cast<float4v*>(&lds_acc[wave][n][i * 16 + 4 * g]) = x;
       }
     }
@@ -444,14 +497,14 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
       float top = -INFINITY, below = 0.0f;
       for (int v = 0; v < W; ++v) top = fmaxf(top, lds_m[v][r]);
       for (int v = 0; v < W; ++v)
-        below += lds_l[v][r] * (lds_m[v][r] == top ? 1.0f : __builtin_amdgcn_exp2f(lds_m[v][r] - top));
+        below += rebase(lds_l[v][r], lds_m[v][r], top);
       if (r0 + r >= packed) continue;
       if (rg.used > 1) {
         put2(part + (at + r) * D + d, sum[0], sum[1]);
         put2(part + (at + r) * D + d + 2, sum[2], sum[3]);
         if (d == 0) put2(part_ml + (at + r) * 2, top, below);
       } else {
-        store_row(r, d, sum, below);
+        store_row<D>(a, sp, head, G, bf16, r0 + r, d, sum, below);
       }
     }
     __syncthreads();
@@ -502,12 +555,12 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
         float keep = ml[j][0] == top ? 1.0f : __builtin_amdgcn_exp2f(ml[j][0] - top);
         if (i0 + j * parts < rg.used) {
           sum += float4v{lo[j][0], lo[j][1], hi[j][0], hi[j][1]} * keep;
-          below += ml[j][1] * keep;
+          below += rebase(ml[j][1], ml[j][0], top);
         }
       }
     }
     if (parts == 1) {
-      store_row(r, x * 4, sum, below);
+      store_row<D>(a, sp, head, G, bf16, r0 + r, x * 4, sum, below);
     } else {
       *reinterpret_cast<float4v*>(lds_flat + (grp * LANES + x) * 4) = sum;
       if (x == 0) lds_l[0][grp] = below;
@@ -522,7 +575,207 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(C
     sum += *reinterpret_cast<const float4v*>(lds_flat + ((grp + i) * LANES + x) * 4);
     below += lds_l[0][grp + i];
   }
-  store_row(grp / parts, x * 4, sum, below);
+  store_row<D>(a, sp, head, G, bf16, r0 + grp / parts, x * 4, sum, below);
+}
+
+constexpr uint32_t kTileRows = 128;
+// Workgroups on a CU: as many as registers and shared memory hold.  3 instead
+// of 2 for one prompt of 4,096 rows of 64 dims: 142 -> 115 us; for 2,048 rows of
+// 96 dims registers spill: 64 -> 94 us.
+constexpr int tiles_occupancy(int D) { return D <= 64 ? 3 : D <= 128 ? 2 : 1; }
+
+// The order of a run of 4 * N reads of shared memory and their 4 * N * NC
+// products: always four reads ahead.
+template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
+  constexpr int kRead = 0x100, kProduct = 0x8;
+  __builtin_amdgcn_sched_group_barrier(kRead, N > 1 ? 8 : 4, 0);
+#pragma unroll
+  for (int i = 0; i < 4 * N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kProduct, NC, 0);
+    if (i + 8 < 4 * N) __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+  }
+}
+
+// Prompts: four waves, 32 rows each, on the same positions.  The same two
+// products as above, but each wave turns a quarter of a step's codes into fp16,
+// once for the four, and shared memory holds them in the order in which the
+// lanes take them, so that every access is one run of 1 KB: while a step is
+// computed the next one's are turned, and those of the one behind it are on
+// their way from memory.  Eight prompts of 4,096 rows behind 4,096 positions (8
+// heads of 128, 32 query heads) 3.6 ms, 915 TFLOP/s, where k_attend_rows takes
+// 4.2 ms: a library product of 8,192 reaches 1,250.  Matrix cores are busy for
+// 35% of the time, vector units for 60%; without exp2 it is as fast, without
+// turning 12% faster, without loads 14%, with an eighth of the second product
+// 10%: the chain of a step (read, product, maximum, exp2, product) is longer
+// than two waves a SIMD hide.
+//
+template <bool E4M3, int D>
+__global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
+                                                                          AttendArgs a, bool bf16, uint32_t units,
+                                                                          uint32_t per_head) {
+  constexpr int NC = 2, WR = 16 * NC, R = kTileRows, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16, VL = (DB + 3) / 4;
+  __shared__ half8 lds[2][(KS * 4 + DB * 2) * 64];  // keys [x][b][lane], values [i][h][lane]
+  __shared__ int lds_nan[2];                        // 1 + the step whose values have a NaN
+  constexpr int kValues = KS * 4;
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint32_t head, unit, split;
+  place(c.heads, 1, per_head, &head, &unit, &split);
+  if (head >= c.heads || unit >= units) return;
+  const uint32_t G = a.q_heads / c.heads;
+  uint32_t seq;
+  Span sp;
+  uint64_t own;
+  const bool mine = locate_unit(c, s, map, unit, WaveCount{s, map, unit}, &seq, &sp, &own);
+  if (!sp.ok && threadIdx.x == 0) report(c, kCacheBadSeq);
+  const uint32_t packed = sp.n * G;
+  if (!mine || own * R >= packed) return;
+  const uint32_t r0 = (uint32_t)own * R, r1 = min(r0 + R, packed);
+  Range rg = range_of(sp, r0 / G, (r1 - 1) / G + 1, a.window, 1, 1);
+  if (!sp.ok || c.pages == 0) {
+    if (sp.ok && threadIdx.x == 0) report(c, kCacheBadPage);
+    rg.hi = rg.lo = rg.steps = 0;
+  }
+  const float base = a.scale * kLog2e;
+  // the wave's rows, the positions that some of them see and those that all see
+  const uint32_t w0 = r0 + wave * WR, w1 = min(w0 + WR, packed);
+  const bool live = w0 < w1 && rg.steps > 0;
+  const int hi = live ? (int)(sp.start + (w1 - 1) / G) + 1 : 0, all_hi = live ? (int)(sp.start + w0 / G) + 1 : 0;
+  const int lo = a.window ? max(all_hi - (int)a.window, 0) : 0, all_lo = a.window ? max(hi - (int)a.window, 0) : 0;
+  Rows<D, NC> w;
+  load_rows<D, NC>(w, a, sp, head, G, w0, packed, bf16, n, g);
+
+  const uint32_t page_mask = (1u << c.page_log) - 1;
+  const int kb = n >> 2;
+  const int32_t* table = s.table + seq * s.table_stride;
+  auto page_of = [&](int t) -> int32_t { return t < rg.hi ? table[(uint32_t)t >> c.page_log] : -1; };
+  auto block_at = [&](int t, int32_t p) -> uint64_t {
+    return head_offset(c, (uint32_t)p < c.pages ? (uint32_t)p : 0, head) + (((uint32_t)t & page_mask) >> 4) * (16 * D);
+  };
+  // a quarter of a step's codes: block b = wave of the keys, dims 16 i + n of the values, i = wave, wave + 4 ..
+  uint4v kr[KL], vr[VL];
+  uint2v kt = {0, 0};
+  int32_t k_page = -1, v_page = -1;           // of the step to load next
+  int32_t page = -1, next_page = -1;          // of the step computed, and of the next one, at g's tokens
+  uint32_t scales = 0, next_scales = 0;
+  auto pages = [&](int step) {
+    k_page = page_of(step * kStep + kb * 16);
+    v_page = page_of(step * kStep + g * 16);
+  };
+  auto load = [&](int step) {
+    const uint8_t* k = c.k + block_at(step * kStep + kb * 16, k_page) + (n & 3) * 16 + wave * 64;
+    const uint8_t* v = c.v + block_at(step * kStep + g * 16, v_page) + n * 16;
+    for (int j = 0; j < KL; ++j) kr[j] = *reinterpret_cast<const uint4v*>(k + g * 256 + j * 1024);
+    if constexpr (TAIL) kt = *reinterpret_cast<const uint2v*>(k + KL * 1024 + (g >> 1) * 256 + (g & 1) * 8);
+    for (int i = 0; i < VL; ++i)
+      if (DB % 4 == 0 || wave + 4 * i < DB) vr[i] = *reinterpret_cast<const uint4v*>(v + (wave + 4 * i) * 256);
+    next_page = v_page;
+    next_scales = *reinterpret_cast<const uint16_t*>(
+        c.scales + ((uint64_t)((uint32_t)v_page < c.pages ? (uint32_t)v_page : 0) * c.heads + head) * 2);
+    pages(step + 1);
+  };
+  auto turn = [&](int step) {
+    half8* to = lds[step & 1] + lane;
+    for (int j = 0; j < KL; ++j)
+      for (int x = 0; x < 2; ++x)
+        to[((2 * j + x) * 4 + wave) * 64] = codes_to_half<E4M3>(kr[j][2 * x], kr[j][2 * x + 1]);
+    if constexpr (TAIL) to[((KS - 1) * 4 + wave) * 64] = codes_to_half<E4M3>(kt[0], kt[1]);
+    // values that no row sees may be anything, and 0 * NaN is NaN
+    const int t0 = step * kStep, tv = t0 + g * 16;
+    const bool lost = (uint32_t)next_page >= c.pages;
+    if (t0 < rg.lo || t0 + kStep > rg.hi || __any(lost))
+      for (int dw = 0; dw < 4; ++dw) {
+        const uint32_t keep = lost ? 0 : byte_mask(tv + 4 * dw, rg.lo, rg.hi);
+        for (int i = 0; i < VL; ++i) vr[i][dw] &= keep;
+      }
+    if constexpr (E4M3) {
+      uint32_t any = 0;
+      for (int i = 0; i < VL; ++i)
+        for (int dw = 0; dw < 4; ++dw) any |= nan_bytes(vr[i][dw]);
+      if (__any(any != 0)) {
+        for (int i = 0; i < VL; ++i)
+          for (int dw = 0; dw < 4; ++dw) vr[i][dw] = without_nan(vr[i][dw]);
+        if (lane == 0) lds_nan[step & 1] = step + 1;
+      }
+    }
+    for (int i = 0; i < VL; ++i)
+      if (DB % 4 == 0 || wave + 4 * i < DB)
+        for (int h = 0; h < 2; ++h)
+          to[(kValues + 2 * (wave + 4 * i) + h) * 64] = codes_to_half<E4M3>(vr[i][2 * h], vr[i][2 * h + 1]);
+  };
+
+  int step = rg.first;
+  const int step_end = rg.first + rg.steps;
+  for (int i = 0; i < VL; ++i) vr[i] = uint4v{0, 0, 0, 0};
+  if (threadIdx.x < 2) lds_nan[threadIdx.x] = 0;
+  __syncthreads();
+  if (step < step_end) {
+    pages(step);
+    load(step);
+    turn(step);
+    page = next_page;
+    scales = next_scales;
+    if (step + 1 < step_end) load(step + 1);
+  }
+  for (; step < step_end; ++step) {
+    __syncthreads();  // the step's values are there, and the other buffer is not read any more
+    const int32_t p_now = page;
+    const bool have = (uint32_t)p_now < c.pages;
+    const uint32_t sc = scales;
+    if (step + 1 < step_end) {
+      turn(step + 1);
+      page = next_page;
+      scales = next_scales;
+      if (step + 2 < step_end) load(step + 2);
+    }
+    const int t0 = step * kStep, tv = t0 + g * 16;
+    if (t0 >= hi || t0 + kStep <= lo) continue;
+    const half8* from = lds[step & 1] + lane;
+    // ---- S^T; no two products in a row on the same sums, four reads ahead
+    float4v st[NC][4];
+    for (int nc = 0; nc < NC; ++nc)
+      for (int b = 0; b < 4; ++b) st[nc][b] = float4v{0, 0, 0, 0};
+#pragma unroll
+    for (int x = 0; x < KS; ++x)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const half8 k8 = from[(x * 4 + b) * 64];
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+          st[nc][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w.q[nc][x], st[nc][b], 0, 0, 0);
+      }
+    reads_ahead<KS, NC>();
+    // ---- weights
+    const bool lost = tv < hi && tv + 16 > lo && !have;
+    if (lost && n == 0) report(c, kCacheBadPage);
+    const bool edge = t0 < all_lo || t0 + kStep > all_hi || __any(lost);
+    half8 p[NC][2];
+    step_weights<D, NC>(w, st, p, base, sc, tv, edge, have);
+    // ---- O^T
+    from += kValues * 64;
+#pragma unroll
+    for (int i = 0; i < DB; i += 2)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = i; j < i + 2; ++j) {
+          const half8 v8 = from[(2 * j + h) * 64];
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc)
+            w.acc[nc][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p[nc][h], w.acc[nc][j], 0, 0, 0);
+        }
+    reads_ahead<DB / 2, NC>();
+    if (E4M3 && lds_nan[step & 1] == step + 1) note_nan<D, NC>(w, tv, have, c.v + block_at(tv, p_now) + n * 16);
+  }
+  if constexpr (E4M3) apply_nan<D, NC>(w);
+  for (int nc = 0; nc < NC; ++nc) {
+    float below = w.l[nc];
+    below += __shfl_xor(below, 16);
+    below += __shfl_xor(below, 32);
+    const uint32_t r = w0 + nc * 16 + n;
+    if (r < packed)
+      for (int i = 0; i < DB; ++i) store_row<D>(a, sp, head, G, bf16, r, i * 16 + 4 * g, w.acc[nc][i], below);
+  }
 }
 
 constexpr int kWaves = 4;
@@ -536,6 +789,7 @@ struct Plan {
   UnitMap map;
   uint32_t units, nc, splits;
   uint32_t per_head;  // workgroups of a head
+  bool tiles;
   dim3 grid;
 };
 
@@ -543,8 +797,17 @@ Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t 
   Plan p;
   const uint32_t G = q_heads / c.heads;
   const uint64_t mean = ((uint64_t)s.rows * G + s.seqs - 1) / s.seqs;  // packed rows of a sequence and head
+  // k_attend_tiles where there are workgroups for all CUs and rows to fill its
+  // tiles, else k_attend_rows, which splits the positions.  tiles / rows: one
+  // prompt of 512, 1,024, 2,048 and of 16 times 2,048 rows (8 heads of 128, 4
+  // query heads each) 24 / 15, 38 / 31, 72 / 76 and 778 / 1,216 us; of 1,024 rows
+  // of 256 dims 74 / 108 us.  With 1,000 positions before them, 100 times 32 rows
+  // (128 packed) 193 / 154 us, 200 times 16 (64 packed) of 64 dims 111 / 208 us.
+  const uint64_t tiles = unit_count(UnitMap{G, kTileRows, 1}, s.rows, s.seqs) * c.heads;
+  p.tiles = s.cu && mean + 64 >= 2 * c.dim && tiles >= (c.dim <= 128 ? 512 : 256);
+  // more rows a wave where they are there and registers hold them
   p.nc = mean <= 16 || c.dim > 192 ? 1 : mean <= 32 || c.dim > 96 ? 2 : 4;
-  const uint32_t R = 16 * p.nc;
+  const uint32_t R = p.tiles ? kTileRows : 16 * p.nc;
   p.map = s.cu ? UnitMap{G, R, 1} : UnitMap{0, 1, (G + R - 1) / R};
   p.units = (uint32_t)unit_count(p.map, s.rows, s.seqs);
   uint64_t longest = (uint64_t)s.width << c.page_log;
@@ -553,7 +816,7 @@ Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t 
   const uint64_t base = (uint64_t)p.units * c.heads;
   const uint64_t want = (kFill + base - 1) / base;
   p.splits = (uint32_t)(want < most ? want : most);
-  if (p.splits < 1 || base > kCounters) p.splits = 1;
+  if (p.splits < 1 || base > kCounters || p.tiles) p.splits = 1;
   const uint32_t share = chiplet_share(c.heads);
   p.per_head = (p.units * p.splits + share - 1) / share * share;
   const uint64_t groups = (uint64_t)p.per_head * c.heads;  // a multiple of 8
@@ -565,6 +828,10 @@ template <bool E4M3, int D>
 hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
                        hipStream_t st) {
   constexpr int T = 64 * kWaves;
+  if (p.tiles) {
+    k_attend_tiles<E4M3, D><<<p.grid, 256, 0, st>>>(c, s, p.map, a, bf16, p.units, p.per_head);
+    return hipGetLastError();
+  }
   if (p.nc == 1) k_attend_rows<E4M3, D, 1, kWaves><<<p.grid, T, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
   else if constexpr (D <= 192) {
     if (p.nc == 2) k_attend_rows<E4M3, D, 2, kWaves><<<p.grid, T, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
