@@ -456,7 +456,8 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
  * power-of-two scale for each page, head and kind (key, value):
  *   k_codes u8 [pages][heads][page/16][dim/16][16 tokens][16 dims]
  *   v_codes u8 [pages][heads][page/16][dim][16 tokens]
- *   scales  u8 [pages][heads][2] (key, value); a scale is 2^(byte - 127), byte 1..254
+ *   scales  u8 [pages][heads][2] (key, value); a scale is 2^(byte - 127), byte
+ *           27..247 (what ltc_cache_write stores: 2^-100 to 2^120)
  * Codes are OCP E4M3 (LTC_E4M3) or two's-complement integers (LTC_INT8); a
  * number is its code times its scale.  The layouts are those in which the
  * matrix cores take 16 tokens of keys and values.
@@ -476,7 +477,7 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
  * The status is only ever added to; a caller clears it when it has read it.
  *
  * Argument errors that the host sees (types, sizes, null or misaligned
- * pointers, a grid past the device's limits) return before anything is
+ * pointers, more than 2^24 rows or 2^20 sequences) return before anything is
  * enqueued.  A call without rows or sequences succeeds and does nothing. */
 enum { LTC_E4M3 = 0, LTC_INT8 = 1 };
 enum { LTC_CACHE_BAD_PAGE = 1, LTC_CACHE_BAD_SEQUENCE = 2 };
@@ -528,7 +529,11 @@ int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k
  * positions the rows are: the row at position p sees positions t <= p, and with
  * window > 0 only t > p - window.  Query head h reads head h / (q_heads /
  * heads).  d_out [rows][q_heads][dim] (16-byte aligned) gets
- * softmax(scale * q k^T) v, zeros for a row that sees nothing.  The workspace
+ * softmax(scale * q k^T) v, zeros for a row that sees nothing.  (rows + seqs) *
+ * q_heads may be 2^31 at most.  A NaN among the keys or values that a row sees
+ * makes it NaN (a value's, in its dim alone); what it does not see has no part
+ * in it.  Weights are rounded to fp16 before they meet the values, sums are held
+ * in fp32.  A result depends on the call's shapes, not on timing.  The workspace
  * has ltc_cache_attend_workspace_size() bytes, 256-byte aligned (none may be
  * needed, then d_ws may be NULL).  Its first LTC_CACHE_WS_ZEROS bytes must be
  * zero before the first call that uses it, and every call leaves them zero: a

@@ -9,6 +9,8 @@
 // below the fraction gathers u_t 2^-w: so the weights that multiply the codes
 // stay near one whatever the pages' scales are, and the codes go into the
 // matrix cores as they are.
+#include <type_traits>
+
 #include "ltc_cache_device.h"
 
 namespace ltc {
@@ -520,62 +522,82 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   if (threadIdx.x == 0) lds_last = atomicInc(static_cast<uint32_t*>(a.ws) + tile, (uint32_t)rg.used - 1) + 1 == (uint32_t)rg.used;
   __syncthreads();
   if (!lds_last) return;
-  constexpr int LANES = D / 4, GROUPS = 64 * W / LANES, kAhead = 8;
+  constexpr int LANES = D / 4, GROUPS = 64 * W / LANES;
   const int grp = threadIdx.x / LANES, x = threadIdx.x % LANES;
   const uint64_t at0 = tile * splits * R;
   const int live = (int)min(packed - r0, (uint32_t)R);
   // the rows' bounds, then their weighted sums: a group of lanes takes rows
   // whole, or, where there are fewer rows than groups, a row's every
   // parts-th split
-  for (int r = wave; r < live; r += W) {
+  const int width = rg.used <= 4 ? 4 : rg.used <= 16 ? 16 : 64;  // lanes of a row
+  for (int r = threadIdx.x / width; r < live; r += 64 * W / width) {
     float top = -INFINITY;
-    for (int i = lane; i < rg.used; i += 64) top = fmaxf(top, get2(part_ml + (at0 + (uint64_t)i * R + r) * 2)[0]);
-    for (int v = 32; v; v >>= 1) top = fmaxf(top, __shfl_xor(top, v));
-    if (lane == 0) lds_m[0][r] = top;
+    for (int i = lane % width; i < rg.used; i += width) top = fmaxf(top, get2(part_ml + (at0 + (uint64_t)i * R + r) * 2)[0]);
+    for (int v = width / 2; v; v >>= 1) top = fmaxf(top, __shfl_xor(top, v));
+    if (lane % width == 0) lds_m[0][r] = top;
   }
   __syncthreads();
+  // RA rows' SA splits at once: they come from beyond the L2
+  auto gather = [&](auto ra, auto sa, int first, int dr, int i0, int di, float4v* sum, float* below) {
+    constexpr int RA = decltype(ra)::value, SA = decltype(sa)::value;
+    float top[RA];
+    for (int k = 0; k < RA; ++k) {
+      sum[k] = float4v{0, 0, 0, 0};
+      below[k] = 0.0f;
+      top[k] = lds_m[0][min(first + k * dr, live - 1)];
+    }
+    for (int i = i0; i < rg.used; i += SA * di) {
+      float2v ml[RA][SA], lo[RA][SA], hi[RA][SA];
+#pragma unroll
+      for (int k = 0; k < RA; ++k)
+#pragma unroll
+        for (int j = 0; j < SA; ++j) {
+          const uint64_t p = at0 + (uint64_t)min(i + j * di, rg.used - 1) * R + min(first + k * dr, live - 1);
+          ml[k][j] = get2(part_ml + p * 2);
+          lo[k][j] = get2(part + p * D + x * 4);
+          hi[k][j] = get2(part + p * D + x * 4 + 2);
+        }
+#pragma unroll
+      for (int k = 0; k < RA; ++k)
+#pragma unroll
+        for (int j = 0; j < SA; ++j)
+          if (i + j * di < rg.used) {
+            const float keep = ml[k][j][0] == top[k] ? 1.0f : __builtin_amdgcn_exp2f(ml[k][j][0] - top[k]);
+            sum[k] += float4v{lo[k][j][0], lo[k][j][1], hi[k][j][0], hi[k][j][1]} * keep;
+            below[k] += rebase(ml[k][j][1], ml[k][j][0], top[k]);
+          }
+    }
+  };
   const int parts = max(GROUPS / live, 1), mine_of = grp % parts;
   float* lds_flat = &lds_acc[0][0][0];
-  for (int r = grp / parts; r < live && grp < GROUPS; r += GROUPS / parts) {  // once, if parts > 1
-    const float top = lds_m[0][r];
-    float4v sum = {0, 0, 0, 0};
-    float below = 0.0f;
-    // kAhead splits' loads at once: they come from beyond the L2
-    for (int i0 = mine_of; i0 < rg.used; i0 += kAhead * parts) {
-      float2v ml[kAhead], lo[kAhead], hi[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const uint64_t p = at0 + (uint64_t)min(i0 + j * parts, rg.used - 1) * R + r;
-        ml[j] = get2(part_ml + p * 2);
-        lo[j] = get2(part + p * D + x * 4);
-        hi[j] = get2(part + p * D + x * 4 + 2);
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        float keep = ml[j][0] == top ? 1.0f : __builtin_amdgcn_exp2f(ml[j][0] - top);
-        if (i0 + j * parts < rg.used) {
-          sum += float4v{lo[j][0], lo[j][1], hi[j][0], hi[j][1]} * keep;
-          below += rebase(ml[j][1], ml[j][0], top);
-        }
-      }
+  if (parts == 1) {
+    constexpr int RA = 4;
+    for (int r = grp; r < live && grp < GROUPS; r += RA * GROUPS) {
+      float4v sum[RA];
+      float below[RA];
+      gather(std::integral_constant<int, RA>(), std::integral_constant<int, 4>(), r, GROUPS, 0, 1, sum, below);
+      for (int k = 0; k < RA; ++k)
+        if (r + k * GROUPS < live) store_row<D>(a, sp, head, G, bf16, r0 + r + k * GROUPS, x * 4, sum[k], below[k]);
     }
-    if (parts == 1) {
-      store_row<D>(a, sp, head, G, bf16, r0 + r, x * 4, sum, below);
-    } else {
-      *reinterpret_cast<float4v*>(lds_flat + (grp * LANES + x) * 4) = sum;
-      if (x == 0) lds_l[0][grp] = below;
-    }
+    return;
   }
-  if (parts == 1) return;
+  const int row = grp / parts;
+  if (row < live && grp < GROUPS) {
+    float4v sum[1];
+    float below[1];
+    gather(std::integral_constant<int, 1>(), std::integral_constant<int, 8>(), row, 0, mine_of, parts, sum, below);
+    *reinterpret_cast<float4v*>(lds_flat + (grp * LANES + x) * 4) = sum[0];
+    if (x == 0) lds_l[0][grp] = below[0];
+  }
   __syncthreads();
-  if (mine_of != 0 || grp / parts >= live || grp >= GROUPS) return;
+  if (mine_of != 0 || row >= live || grp >= GROUPS) return;
   float4v sum = {0, 0, 0, 0};
   float below = 0.0f;
   for (int i = 0; i < parts; ++i) {
     sum += *reinterpret_cast<const float4v*>(lds_flat + ((grp + i) * LANES + x) * 4);
     below += lds_l[0][grp + i];
   }
-  store_row<D>(a, sp, head, G, bf16, r0 + grp / parts, x * 4, sum, below);
+  store_row<D>(a, sp, head, G, bf16, r0 + row, x * 4, sum, below);
 }
 
 constexpr uint32_t kTileRows = 128;

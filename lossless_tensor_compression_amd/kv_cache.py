@@ -32,6 +32,8 @@ DIMS = (64, 96, 128, 192, 256)
 BAD_PAGE, BAD_SEQUENCE = 1, 2
 WS_ZEROS = 65536
 
+_INT32 = torch.int32
+_current_gpu = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds a Stream object: 2.7 us a call
 _pack_seqs = struct.Struct("=QQQQIIII").pack      # ltc_cache_seqs
 _pack_rows = struct.Struct("=QQQ").pack           # ltc_cache_rows
@@ -130,48 +132,57 @@ class KVCache:
         return ws.data_ptr(), ws.numel()
 
     def _seqs(self, table, lengths, cu, rows):
-        """ltc_cache_seqs as bytes; what can be seen without the GPU is checked."""
+        """ltc_cache_seqs as bytes; what can be seen without the GPU is checked.
+        Straight code: it is half of a small call's time."""
+        gpu = self._index
+        if not (table.dtype is _INT32 and lengths.dtype is _INT32 and table.get_device() == gpu
+                and lengths.get_device() == gpu and (cu is None or cu.dtype is _INT32 and cu.get_device() == gpu)):
+            raise ValueError("table, lengths and cu must be int32 on the cache's GPU")
+        shape, stride = table.shape, table.stride()
         seqs = lengths.numel()
-        for name, t in (("table", table), ("lengths", lengths), ("cu", cu)):
-            if t is not None and (t.dtype != torch.int32 or t.get_device() != self._index):
-                raise ValueError(f"{name} must be int32 on the cache's GPU")
-        if table.dim() != 2 or table.shape[0] != seqs or lengths.dim() != 1:
+        if len(shape) != 2 or shape[0] != seqs or lengths.dim() != 1:
             raise ValueError("table must be [sequences, pages] and lengths [sequences]")
-        if not lengths.is_contiguous() or (table.stride(1) != 1 and table.shape[1] > 1):
+        width = shape[1]
+        if not lengths.is_contiguous() or (stride[1] != 1 and width > 1):
             raise ValueError("lengths and the rows of table must be contiguous")
         if cu is None:
             if rows != seqs:
                 raise ValueError("without cu there is one row for each sequence")
         elif cu.dim() != 1 or cu.numel() != seqs + 1 or not cu.is_contiguous():
             raise ValueError("cu must be contiguous [sequences + 1]")
-        width = table.shape[1]
-        stride = table.stride(0) if seqs > 1 else width
-        if stride < width:
+        step = stride[0] if seqs > 1 else width
+        if step < width:
             raise ValueError("the rows of table must not overlap")
-        return _pack_seqs(table.data_ptr(), lengths.data_ptr(), 0 if cu is None else cu.data_ptr(), stride,
+        return _pack_seqs(table.data_ptr(), lengths.data_ptr(), 0 if cu is None else cu.data_ptr(), step,
                           seqs, rows, width, 0)
 
     def _rows(self, t, heads, name):
         """t as rows that the kernels can take (a copy where its strides or
-        alignment do not let them) and its ltc_cache_rows as bytes."""
-        if t.dtype != self.dtype or t.get_device() != self._index:
+        alignment do not let them), its ltc_cache_rows as bytes and its shape."""
+        if t.dtype is not self.dtype or t.get_device() != self._index:
             raise ValueError(f"{name} must be {self.dtype} on the cache's GPU")
-        if t.dim() != 3 or t.shape[2] != self.dim or (heads is not None and t.shape[1] != heads):
+        shape = t.shape
+        if len(shape) != 3 or shape[2] != self.dim or (heads is not None and shape[1] != heads):
             raise ValueError(f"{name} must be [rows, {'heads' if heads is None else heads}, {self.dim}]")
         r, h, d = t.stride()
-        if d != 1 or r % 8 or h % 8 or t.data_ptr() % 16:
+        at = t.data_ptr()
+        if d != 1 or r % 8 or h % 8 or at % 16:
             t = t.contiguous() if not t.is_contiguous() else t.clone()
             r, h, d = t.stride()
-        return t, _pack_rows(t.data_ptr(), r, h)
+            at = t.data_ptr()
+        return t, _pack_rows(at, r, h), shape
 
 
 def cache_write(cache, k, v, table, lengths, cu=None):
     """Quantises keys and values [rows, heads, dim] into the cache's pages."""
-    k, kr = cache._rows(k, cache.heads, "k")
-    v, vr = cache._rows(v, cache.heads, "v")
-    if k.shape[0] != v.shape[0]:
+    if _current_gpu() != cache._index:
+        with torch.cuda.device(cache._index):
+            return cache_write(cache, k, v, table, lengths, cu)
+    k, kr, k_shape = cache._rows(k, cache.heads, "k")
+    v, vr, v_shape = cache._rows(v, cache.heads, "v")
+    if k_shape != v_shape:
         raise ValueError("one value row for each key row")
-    s = cache._seqs(table, lengths, cu, k.shape[0])
+    s = cache._seqs(table, lengths, cu, k_shape[0])
     _check(cache._lib.ltc_cache_write(cache._ref, s, kr, vr, _raw_stream(cache._index)), "cache_write")
 
 
@@ -179,6 +190,9 @@ def cache_read(cache, table, lengths, cu=None, rows=None):
     """The keys and values (two tensors [rows, heads, dim] of the cache's
     dtype) at the positions of the call's rows; rows = cu[-1], which only the
     GPU knows, has to be given with cu."""
+    if _current_gpu() != cache._index:
+        with torch.cuda.device(cache._index):
+            return cache_read(cache, table, lengths, cu, rows)
     if rows is None:
         if cu is not None:
             raise ValueError("rows must be given with cu")
@@ -195,8 +209,10 @@ def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None):
     """softmax(scale * q k^T) v of queries [rows, q_heads, dim] over the
     positions up to each row's own (with window: the last `window` of them);
     zeros for a row that sees nothing.  scale is dim^-0.5 by default."""
-    q, qr = cache._rows(q, None, "q")
-    rows, q_heads, dim = q.shape
+    if _current_gpu() != cache._index:
+        with torch.cuda.device(cache._index):
+            return cache_attend(cache, q, table, lengths, cu, window, scale)
+    q, qr, (rows, q_heads, dim) = cache._rows(q, None, "q")
     s = cache._seqs(table, lengths, cu, rows)
     out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
     stream = _raw_stream(cache._index)
