@@ -295,8 +295,11 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Span& sp, u
   *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = out;
 }
 
-// waves for each SIMD that the kernel's registers are to leave room for
-constexpr int rows_occupancy(int D, int NC) { return D * NC <= 128 ? 3 : D * NC <= 256 && D < 256 ? 2 : 1; }
+// Waves for each SIMD that the kernel's registers are to leave room for: as many
+// as they do without spills.  3 instead of 2 for one column block of 128 dims:
+// 64 rows at 1,000-6,000 positions 93 -> 107 us, one at 131,071 57 -> 61 us; 2
+// instead of 1 for 192 dims: 170 -> 207 us.
+constexpr int rows_occupancy(int D, int NC) { return D * NC <= 64 ? 3 : D * NC <= 256 && D < 192 ? 2 : 1; }
 
 // W waves on a tile of 16 * NC packed rows (row r of a sequence and key head
 // is token r / G, query head r % G of the head's G) and one split of its
@@ -801,10 +804,11 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
 }
 
 constexpr int kWaves = 4;
-// Workgroups that the splits are to make: two for each CU.  One row at 131,071
-// positions with 256 / 512 / 768 / 1024 of them: 64 / 61 / 67 / 75 us; 16
-// sequences of 5 rows: 39 / 33 / 41 / 43 us.  More read faster and join slower.
-constexpr uint32_t kFill = 512;
+// Workgroups that the splits are to make: two for each CU, one where a CU holds
+// one.  One row at 131,071 positions (D = 128) with 256 / 512 / 768 / 1024 of
+// them: 64 / 61 / 67 / 75 us; 16 sequences of 5 rows: 39 / 29 / 39 / 41 us; four
+// rows at 20,001 positions of 2 heads of 256 dims with 256 / 512: 46 / 78 us.
+constexpr uint32_t fill(int D, int NC) { return 256 * (rows_occupancy(D, NC) < 2 ? 1 : 2); }
 constexpr uint32_t kGridWidth = 1u << 20;  // times a workgroup's lanes below 2^32
 
 struct Plan {
@@ -836,7 +840,7 @@ Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t 
   if (window && window + 64 < longest) longest = window + 64;
   const uint64_t most = (longest + kStep * kWaves - 1) / (kStep * kWaves);
   const uint64_t base = (uint64_t)p.units * c.heads;
-  const uint64_t want = (kFill + base - 1) / base;
+  const uint64_t want = (fill((int)c.dim, (int)p.nc) + base - 1) / base;
   p.splits = (uint32_t)(want < most ? want : most);
   if (p.splits < 1 || base > kCounters || p.tiles) p.splits = 1;
   const uint32_t share = chiplet_share(c.heads);
