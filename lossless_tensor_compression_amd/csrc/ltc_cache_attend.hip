@@ -850,20 +850,36 @@ Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t 
   return p;
 }
 
+template <bool E4M3, int D, int W>
+hipError_t launch_waves(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
+                        hipStream_t st) {
+  auto launch = [&](auto kernel) {
+    kernel<<<p.grid, 64 * W, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
+  };
+  if (p.nc == 1) launch(k_attend_rows<E4M3, D, 1, W>);
+  else if constexpr (D <= 192) {
+    if (p.nc == 2) launch(k_attend_rows<E4M3, D, 2, W>);
+    else if constexpr (D <= 96) launch(k_attend_rows<E4M3, D, 4, W>);
+  }
+  return hipGetLastError();
+}
+
 template <bool E4M3, int D>
 hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
                        hipStream_t st) {
-  constexpr int T = 64 * kWaves;
   if (p.tiles) {
     k_attend_tiles<E4M3, D><<<p.grid, 256, 0, st>>>(c, s, p.map, a, bf16, p.units, p.per_head);
     return hipGetLastError();
   }
-  if (p.nc == 1) k_attend_rows<E4M3, D, 1, kWaves><<<p.grid, T, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
-  else if constexpr (D <= 192) {
-    if (p.nc == 2) k_attend_rows<E4M3, D, 2, kWaves><<<p.grid, T, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
-    else if constexpr (D <= 96) k_attend_rows<E4M3, D, 4, kWaves><<<p.grid, T, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
+  // Heads of 192 and 256 dims leave a SIMD one wave: where nothing is split, two
+  // workgroups of two waves hide each other's beginnings and ends.  2 / 4 waves:
+  // 9 prompts of 33-517 rows of 256 dims 47 / 65 us, 300 rows at 10-900 positions
+  // 143 / 176 us, 64 at 1,000-6,000 194 / 192 us.  With 128 dims: 62 / 72 us and
+  // 113 / 92 us, so four there.
+  if constexpr (D >= 192) {
+    if (p.splits == 1) return launch_waves<E4M3, D, 2>(c, s, bf16, a, p, st);
   }
-  return hipGetLastError();
+  return launch_waves<E4M3, D, kWaves>(c, s, bf16, a, p, st);
 }
 
 template <bool E4M3>
