@@ -88,7 +88,7 @@ constexpr uint64_t kCounterBytes = kCounters * 4;
 // accesses of the device's scope, which go past the chiplet's own L2.  The
 // writer's are waited for (wait_stores) before its counter is raised, so no
 // fence has to write an L2 back: with __threadfence() in every workgroup the
-// call of 64 rows at 1,000-6,000 positions took 462 us instead of 115.
+// call of 64 rows at 1,000-6,000 positions took 462 us where it took 115.
 __device__ __forceinline__ void put2(float* p, float a, float b) {
   const float2v x = {a, b};
   __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, x), __ATOMIC_RELAXED,
@@ -316,7 +316,10 @@ constexpr int rows_occupancy(int D, int NC) { return D * NC <= 64 ? 3 : D * NC <
 // Q's does too), values 16 tokens of a dim a lane; a load instruction covers
 // whole 64- and 256-byte runs.  The next step's keys are loaded once this
 // step's are used up, and so for values, so one step (2 * 64 * D bytes) is in
-// flight for each wave.
+// flight for each wave.  Bound by memory where there is enough to read: 64 rows
+// at 1,001-6,001 positions (8 heads of 128, 32 query heads) 91 us, 4.7 TB/s, one
+// at 131,071 57.5 us; by the chain lengths, table, codes, partial results, join
+// where there is not: one at 777 positions 9 us.
 template <bool E4M3, int D, int NC, int W>
 __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16, uint32_t units, uint32_t splits, uint32_t per_head) {
@@ -519,7 +522,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   // ---- the splits' parts together, by the workgroup that comes last (and in
   // the splits' order, so that the order of coming does not matter).  One
   // launch, where a second kernel would cost its launch: for one row at 777
-  // positions 12.8 us a call with it.
+  // positions 12.8 us a call with it, 11 without.
   wait_stores();
   __syncthreads();
   if (threadIdx.x == 0) lds_last = atomicInc(static_cast<uint32_t*>(a.ws) + tile, (uint32_t)rg.used - 1) + 1 == (uint32_t)rg.used;
