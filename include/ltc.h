@@ -470,7 +470,7 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
  * What only the device knows is checked there: a table entry outside
  * [0, pages) below a sequence's length, and lengths or row offsets that
  * contradict each other (offsets that decrease or pass `rows`, more rows than
- * positions, more positions than the table has pages for) set
+ * positions, more positions than the table has pages for, or than 2^30) set
  * LTC_CACHE_BAD_PAGE and LTC_CACHE_BAD_SEQUENCE in *d_status and touch nothing
  * out of bounds: such a page is not written, reads as zeros and is not
  * attended to; such a sequence is not written, and its rows get zeros.

@@ -79,6 +79,26 @@ LTC_HD uint64_t unit_count(const UnitMap& m, uint32_t rows, uint32_t seqs) {
   return (uint64_t)rows * m.mul / m.div + (uint64_t)m.extra * seqs;
 }
 
+// Which head, unit and split workgroup `id` of an attention takes.  Workgroups
+// go to the eight chiplets in turn, and a chiplet's L2 holds what its workgroups
+// read: so the heads are shared out over the chiplets, as far as a power of two
+// divides them, and chiplets that have heads in common take every share-th of
+// their units.  The last units come first: a long prompt's last rows see the
+// most.  share divides per_head, the units times splits of a head and a few
+// numbers without work (unit too large; head too large behind them all).
+LTC_HD uint32_t chiplet_share(uint32_t heads) {
+  return heads % 8 == 0 ? 1 : heads % 4 == 0 ? 2 : heads % 2 == 0 ? 4 : 8;
+}
+LTC_HD void place(uint32_t id, uint32_t heads, uint32_t splits, uint32_t per_head, uint32_t* head, uint32_t* unit,
+                  uint32_t* split) {
+  const uint32_t share = chiplet_share(heads), classes = 8 / share;
+  const uint32_t chiplet = id % 8, i = id / 8 * share + chiplet / classes;
+  *head = chiplet % classes + i / per_head * classes;
+  const uint32_t x = per_head - 1 - i % per_head;
+  *unit = x / splits;
+  *split = x % splits;
+}
+
 // The last sequence whose units begin at or before `unit`, in steps of 64:
 // count(lo, step, n) says at how many of lo, lo + step, ... (64 at most, below
 // lo + n) first() is at most `unit`; on the GPU a wave asks all 64 at once.
@@ -95,9 +115,14 @@ LTC_HD uint32_t find_sequence(uint32_t seqs, Count count) {
   return lo;
 }
 
+// Positions stay below 2^30, so that sums of them and steps past the end fit
+// 32 bits.
+constexpr uint64_t kMaxPositions = 1u << 30;
+
 LTC_HD Span load_span(const CacheView& c, const SeqView& s, uint32_t seq) {
   const int32_t c0 = s.cu ? s.cu[seq] : (int32_t)seq, c1 = s.cu ? s.cu[seq + 1] : (int32_t)seq + 1;
-  return span_of(c0, c1, s.lengths[seq], s.rows, (uint64_t)s.width << c.page_log);
+  const uint64_t capacity = (uint64_t)s.width << c.page_log;
+  return span_of(c0, c1, s.lengths[seq], s.rows, capacity < kMaxPositions ? capacity : kMaxPositions);
 }
 
 LTC_HD uint64_t unit_first(const UnitMap& m, const SeqView& s, uint32_t seq) {

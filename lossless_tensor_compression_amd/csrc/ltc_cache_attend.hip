@@ -106,27 +106,6 @@ __device__ __forceinline__ uint32_t pack2_as(bool bf16, float a, float b) {
   return bf16 ? pack2<LTC_BF16>(a, b) : pack2<LTC_FP16>(a, b);
 }
 
-// Which head, unit and split a workgroup takes.  Workgroups go to the eight
-// chiplets in turn, and a chiplet's L2 holds what its workgroups read: so the
-// heads are shared out over the chiplets, as far as a power of two divides
-// them, and chiplets that have heads in common take every share-th of their
-// units.  The last units come first: a long prompt's last rows see the most.
-// share divides per_head, the units times splits of a head and a few numbers
-// without work.
-__host__ __device__ constexpr uint32_t chiplet_share(uint32_t heads) {
-  return heads % 8 == 0 ? 1 : heads % 4 == 0 ? 2 : heads % 2 == 0 ? 4 : 8;
-}
-__device__ __forceinline__ void place(uint32_t heads, uint32_t splits, uint32_t per_head, uint32_t* head,
-                                      uint32_t* unit, uint32_t* split) {
-  const uint32_t id = blockIdx.x + gridDim.x * blockIdx.y;
-  const uint32_t share = chiplet_share(heads), classes = 8 / share;
-  const uint32_t chiplet = id % 8, i = id / 8 * share + chiplet / classes;
-  *head = chiplet % classes + i / per_head * classes;
-  const uint32_t x = per_head - 1 - i % per_head;
-  *unit = x / splits;
-  *split = x % splits;
-}
-
 // A denominator's part from one bound to another.  Where pages' scales lie far
 // apart it may be large while 2^(from - to) is below fp32's numbers: so that
 // comes in two halves.
@@ -329,7 +308,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   __shared__ bool lds_last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
   uint32_t head, unit, split;
-  place(c.heads, splits, per_head, &head, &unit, &split);
+  place(blockIdx.x + gridDim.x * blockIdx.y, c.heads, splits, per_head, &head, &unit, &split);
   if (head >= c.heads || unit >= units) return;
   const uint32_t G = a.q_heads / c.heads;
   uint32_t seq;
@@ -648,7 +627,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t head, unit, split;
-  place(c.heads, 1, per_head, &head, &unit, &split);
+  place(blockIdx.x + gridDim.x * blockIdx.y, c.heads, 1, per_head, &head, &unit, &split);
   if (head >= c.heads || unit >= units) return;
   const uint32_t G = a.q_heads / c.heads;
   uint32_t seq;

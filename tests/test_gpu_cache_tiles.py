@@ -113,3 +113,31 @@ def test_queries_far_below_one(ltc):  # noqa: F811
     want, slack, _ = co.attend(s.o, q64, s.table, s.lengths, s.cu)
     close(out, want, slack, BF)
     assert len(np.unique(want.round(3))) > 100
+
+
+def test_more_positions_than_a_sequence_may_have(ltc):  # noqa: F811
+    """A table for more than 2^30 positions, all on one page: lengths past that
+    are refused on the device, shorter ones are served."""
+    s = Setup(ltc, 71, 1, 64, 256, "e4m3", BF, [1, 1, 1], [299, 40, 9], nan_behind=False, single=True)
+    wide = torch.zeros((3, (1 << 22) + 5), dtype=torch.int32, device="cuda")
+    wide[:, :s.gtable.shape[1]] = s.gtable
+    lengths = torch.tensor([300, (1 << 30) + 1, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    q, _ = s.rows16(2)
+    out = ltc.cache_attend(s.cache, q, wide, lengths)
+    want = ltc.cache_attend(s.cache, q[:1], s.gtable[:1], lengths[:1])
+    assert not out[1:].any() and int(s.cache.status.item()) == 2
+    assert (out[0].float() - want[0].float()).abs().max() <= 2.0 ** -7 * want.abs().max()
+    k, v = ltc.cache_read(s.cache, wide, lengths)
+    assert not k[1:].any() and not v[1:].any() and k[0].any()
+
+
+def test_no_pages(ltc):  # noqa: F811
+    cache = ltc.KVCache.empty(0, 2, 64, page=16)
+    x = torch.ones((3, 2, 64), dtype=BF, device="cuda")
+    table = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    lengths, cu = torch.tensor([9], dtype=torch.int32, device="cuda"), torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    ltc.cache_write(cache, x, x, table, lengths, cu)
+    assert not ltc.cache_attend(cache, x, table, lengths, cu).any()
+    assert not ltc.cache_read(cache, table, lengths, cu, rows=3)[0].any()
+    with pytest.raises(ltc.LTCError):
+        cache.check()
