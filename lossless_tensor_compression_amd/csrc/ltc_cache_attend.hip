@@ -807,14 +807,17 @@ Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t 
   const uint64_t mean = ((uint64_t)s.rows * G + s.seqs - 1) / s.seqs;  // packed rows of a sequence and head
   // k_attend_tiles where there are workgroups for all CUs and rows to fill its
   // tiles, else k_attend_rows, which splits the positions.  tiles / rows: one
-  // prompt of 512, 1,024, 2,048 and of 16 times 2,048 rows (8 heads of 128, 4
-  // query heads each) 24 / 15, 38 / 31, 72 / 76 and 778 / 1,216 us; of 1,024 rows
-  // of 256 dims 74 / 108 us.  With 1,000 positions before them, 100 times 32 rows
-  // (128 packed) 193 / 154 us, 200 times 16 (64 packed) of 64 dims 111 / 208 us.
+  // prompt of 512, 1,024, 2,048 and 16 of 2,048 rows (8 heads of 128, 4 query
+  // heads each) 24 / 15, 38 / 31, 72 / 76 and 778 / 1,216 us; two of 1,024 rows of
+  // 256 dims 96 / 145 us.  100 times 64 and 96 packed rows of 64 dims behind 1,000
+  // positions 76 / 62 and 78 / 99 us, 100 times 128 and 192 of 128 dims 182 / 136
+  // and 189 / 213 us.
   const uint64_t tiles = unit_count(UnitMap{G, kTileRows, 1}, s.rows, s.seqs) * c.heads;
-  p.tiles = s.cu && mean + 64 >= 2 * c.dim && tiles >= (c.dim <= 128 ? 512 : 256);
-  // more rows a wave where they are there and registers hold them
-  p.nc = mean <= 16 || c.dim > 192 ? 1 : mean <= 32 || c.dim > 96 ? 2 : 4;
+  p.tiles = s.cu && mean > (c.dim <= 96 ? 64 : 128) && tiles >= (c.dim <= 128 ? 512 : 256);
+  // Two column blocks a wave where there are rows for them; four leave a SIMD one
+  // wave: 80 times 10 rows (40 packed) of 96 dims 106 / 161 us with two / four, 20
+  // times 16 of 64 dims 29 / 47 us, and two instead of one of 256 dims 76 / 65 us.
+  p.nc = mean <= 16 || c.dim > 192 ? 1 : 2;
   const uint32_t R = p.tiles ? kTileRows : 16 * p.nc;
   p.map = s.cu ? UnitMap{G, R, 1} : UnitMap{0, 1, (G + R - 1) / R};
   p.units = (uint32_t)unit_count(p.map, s.rows, s.seqs);
@@ -839,10 +842,7 @@ hipError_t launch_waves(const CacheView& c, const SeqView& s, bool bf16, const A
     kernel<<<p.grid, 64 * W, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
   };
   if (p.nc == 1) launch(k_attend_rows<E4M3, D, 1, W>);
-  else if constexpr (D <= 192) {
-    if (p.nc == 2) launch(k_attend_rows<E4M3, D, 2, W>);
-    else if constexpr (D <= 96) launch(k_attend_rows<E4M3, D, 4, W>);
-  }
+  else if constexpr (D <= 192) launch(k_attend_rows<E4M3, D, 2, W>);
   return hipGetLastError();
 }
 

@@ -30,7 +30,7 @@ def setup(ltc, name, seed, **kw):  # noqa: F811
     before = [int(rng.integers(past[0], past[1] + 1)) for _ in range(n)]
     new[1], before[2] = 0, 0
     new[0] += rows[1]
-    assert sum(new) * G // n + 64 >= 2 * D and (sum(new) * G // 128 + n) * H >= (512 if D <= 128 else 256)
+    assert sum(new) * G // n > (64 if D <= 96 else 128) and (sum(new) * G // 128 + n) * H >= (512 if D <= 128 else 256)
     return Setup(ltc, seed, H, D, P, codes, dtype, new, before, **kw), H * G
 
 
