@@ -296,7 +296,7 @@ constexpr int rows_occupancy(int D, int NC) { return D * NC <= 64 ? 3 : D * NC <
 // whole 64- and 256-byte runs.  The next step's keys are loaded once this
 // step's are used up, and so for values, so one step (2 * 64 * D bytes) is in
 // flight for each wave.  Bound by memory where there is enough to read: 64 rows
-// at 1,001-6,001 positions (8 heads of 128, 32 query heads) 91 us, 4.7 TB/s, one
+// at 1,001-6,001 positions (8 heads of 128, 32 query heads) 93 us, 4.6 TB/s, one
 // at 131,071 57.5 us; by the chain lengths, table, codes, partial results, join
 // where there is not: one at 777 positions 9 us.
 template <bool E4M3, int D, int NC, int W>
@@ -615,7 +615,6 @@ template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
 // turning 12% faster, without loads 14%, with an eighth of the second product
 // 10%: the chain of a step (read, product, maximum, exp2, product) is longer
 // than two waves a SIMD hide.
-//
 template <bool E4M3, int D>
 __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
                                                                           AttendArgs a, bool bf16, uint32_t units,
