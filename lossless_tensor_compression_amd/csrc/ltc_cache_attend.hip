@@ -7,8 +7,8 @@
 // The weights u_t = 2^(x_t + w - m) carry the values' scale, m is a running
 // bound of x_t + w (not below its maximum by more than kSlack), and the sum
 // below the fraction gathers u_t 2^-w: so the weights that multiply the codes
-// stay near one whatever the pages' scales are, and the codes go into the
-// matrix cores as they are.
+// have one range whatever the pages' scales are, and the codes go into the
+// matrix cores as they are.  The matrix cores get 2^kHead u_t, rounded to fp16.
 #include <type_traits>
 
 #include "ltc_cache_device.h"
@@ -19,10 +19,16 @@ namespace {
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-// A tile whose largest x + w is within 2^kSlack of the running bound keeps the
-// bound: weights up to 2^kSlack are as exact in fp16 as those up to 1, and the
-// accumulators are seldom scaled.
-constexpr float kSlack = 6.0f;
+// A step whose largest x + w is within kSlack of the running bound keeps the
+// bound, so the accumulators are seldom scaled.
+constexpr int kSlack = 6;
+// Weights meet the codes times 2^kHead, which puts the largest at 2^15, below
+// fp16's top.  A position that takes nearly all of the weight may have values
+// near zero, and then the output is what thousands of far smaller weights make
+// of theirs: these keep 11 bits down to 2^-(14 + kHead) of the bound and are lost
+// at 2^-(25 + kHead).  kSlack 6 / 4 / 2 / 1: two prompts of 2,500-4,096 rows 648 /
+// 652 / 657 / 661 us, others the same.
+constexpr int kHead = 15 - kSlack;
 
 // Eight codes (two dwords) as fp16, exactly: E4M3 has 3 bits of mantissa and
 // exponents down to 2^-9, INT8 7 bits.
@@ -176,7 +182,7 @@ template <int D, int NC>
 __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], float base,
                                              uint32_t sc, int tv, bool edge, bool have) {
   const int ke = (int)(sc & 0xff) - 127, we = (int)(sc >> 8) - 127;
-  const float wv = (float)we;
+  const float wv = (float)we, wh = (float)(we + kHead);
 #pragma unroll
   for (int nc = 0; nc < NC; ++nc) {
     // not 0: hidden scores are -infinity
@@ -212,7 +218,7 @@ __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4
       lift = rebase(lift, top, w.m[nc] + wv);
     }
     // nothing seen yet: every weight is 0
-    const float shift = w.m[nc] == -INFINITY ? 0.0f : wv - w.m[nc];
+    const float shift = w.m[nc] == -INFINITY ? 0.0f : wh - w.m[nc];
     float sum = 0.0f;
     for (int b = 0; b < 4; ++b)
       for (int i = 0; i < 4; ++i) {
@@ -220,7 +226,7 @@ __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4
         sum += u;
         p[nc][b >> 1][(b & 1) * 4 + i] = (_Float16)u;
       }
-    sum = __builtin_amdgcn_ldexpf(sum, -we);
+    sum = __builtin_amdgcn_ldexpf(sum, -we - kHead);
     w.l[nc] += tiny ? lift : sum;
   }
 }
@@ -264,12 +270,12 @@ template <int D, int NC> __device__ __forceinline__ void apply_nan(Rows<D, NC>& 
 
 __device__ __forceinline__ uint32_t without_nan(uint32_t x) { return x & ~((nan_bytes(x) >> 7) * 0xffu); }
 
-// dims d..d+3 of row r of the sequence and head
+// dims d..d+3 of row r of the sequence and head; sum is 2^kHead times the numerator
 template <int D>
 __device__ __forceinline__ void store_row(const AttendArgs& a, const Span& sp, uint32_t head, uint32_t G, bool bf16,
                                           uint32_t r, int d, float4v sum, float below) {
   const uint32_t token = r / G, qh = head * G + r % G;
-  const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * (1.0f / below);
+  const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * (power_of_two(-kHead) / below);
   const uint2v out = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
   *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = out;
 }
