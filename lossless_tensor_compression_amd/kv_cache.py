@@ -10,7 +10,8 @@ A binding over ltc_cache_write, ltc_cache_read and ltc_cache_attend of
 include/ltc.h, where the layouts, the rounding and what happens with bad
 tables are written down.  Calls run on the current stream, allocate nothing
 but their outputs and a workspace that the cache keeps for each stream, and
-never synchronise, so they can be captured in a graph.
+never synchronise, so they can be captured in a graph.  Threads may share a
+cache; their calls on one stream run in the order in which they are made.
 
 Rows cu[i]..cu[i+1] of a call belong to sequence i and stand for its last
 positions, lengths[i] - (cu[i+1] - cu[i]) to lengths[i] - 1; without cu each
@@ -19,6 +20,7 @@ table[i, t // page].  table, lengths and cu are int32 tensors on the GPU.
 """
 import ctypes
 import struct
+import threading
 
 import torch
 
@@ -76,6 +78,7 @@ class KVCache:
         self._ref = ctypes.byref(self._struct)
         self._index = self.device.index
         self._workspaces = {}  # stream -> tensor, its first bytes zero between calls
+        self._lock = threading.Lock()  # from a workspace's lookup to the launch that uses it
 
     @staticmethod
     def _shape(k_codes, v_codes, scales):
@@ -119,9 +122,10 @@ class KVCache:
             raise LTCError(-5, " and ".join(what))
 
     def _workspace(self, need, stream):
-        """Device pointer and size of a workspace for a call on the stream.
-        Each stream keeps one, since its calls run in order; a captured call
-        gets its own, which lives and is cleared with the graph."""
+        """A workspace for a call on the stream, for the caller to hold until
+        it has launched.  Each stream keeps one, since its calls run in order;
+        a captured call gets its own, which lives and is cleared with the
+        graph."""
         captured = torch._C._cuda_isCurrentStreamCapturing()
         ws = None if captured else self._workspaces.get(stream)
         if ws is None or ws.numel() < need:
@@ -129,7 +133,7 @@ class KVCache:
             ws[:WS_ZEROS].zero_()
             if not captured:
                 self._workspaces[stream] = ws
-        return ws.data_ptr(), ws.numel()
+        return ws
 
     def _seqs(self, table, lengths, cu, rows):
         """ltc_cache_seqs as bytes; what can be seen without the GPU is checked.
@@ -217,7 +221,15 @@ def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None):
     out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
     stream = _raw_stream(cache._index)
     need = cache._lib.ltc_cache_attend_workspace_size(cache._ref, s, q_heads, window)
-    ws, size = cache._workspace(need, stream) if need else (None, 0)
-    _check(cache._lib.ltc_cache_attend(cache._ref, s, qr, q_heads, window, dim ** -0.5 if scale is None else scale,
-                                       out.data_ptr(), ws, size, stream), "cache_attend")
+    scale = dim ** -0.5 if scale is None else scale
+    if not need:
+        _check(cache._lib.ltc_cache_attend(cache._ref, s, qr, q_heads, window, scale, out.data_ptr(), None, 0, stream),
+               "cache_attend")
+        return out
+    # without the lock another thread's call on this stream could replace the
+    # workspace, and its memory could be handed out again before this launch
+    with cache._lock:
+        ws = cache._workspace(need, stream)
+        _check(cache._lib.ltc_cache_attend(cache._ref, s, qr, q_heads, window, scale, out.data_ptr(), ws.data_ptr(),
+                                           ws.numel(), stream), "cache_attend")
     return out
