@@ -171,7 +171,8 @@ class KVCache:
         r, h, d = t.stride()
         at = t.data_ptr()
         if d != 1 or r % 8 or h % 8 or at % 16:
-            t = t.contiguous() if not t.is_contiguous() else t.clone()
+            # a plain clone keeps the strides of dimensions of one, whatever they are
+            t = t.clone(memory_format=torch.contiguous_format)
             r, h, d = t.stride()
             at = t.data_ptr()
         return t, _pack_rows(at, r, h), shape
