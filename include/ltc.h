@@ -465,7 +465,9 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
  * A call's rows belong to sequences: rows cu[i]..cu[i+1] to sequence i, as its
  * last positions, lengths[i] - (cu[i+1] - cu[i]) to lengths[i] - 1.  Position t
  * of a sequence is token t % page of page table[i][t / page].  Without d_cu
- * every sequence has one row.
+ * every sequence has one row.  Rows before cu[0] and from cu[seqs] on belong to
+ * no sequence: they are not written, and where they are outputs they get zeros
+ * (so a captured call of a fixed number of rows may have fewer in use).
  *
  * What only the device knows is checked there: a table entry outside
  * [0, pages) below a sequence's length, and lengths or row offsets that

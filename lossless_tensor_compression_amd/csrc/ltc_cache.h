@@ -59,6 +59,31 @@ LTC_HD Span span_of(int32_t c0, int32_t c1, int32_t length, uint32_t rows, uint6
   return s;
 }
 
+// Rows of the call that belong to no sequence, [0, before) and [behind, rows):
+// a call of a fixed number of rows may have fewer sequences' rows in it.
+struct Unnamed {
+  uint32_t before, behind, n;
+};
+
+// The row offsets that say so, to be loaded early (without branches: they come
+// with other loads).
+struct Ends {
+  int32_t first, last;
+};
+
+LTC_HD Ends load_ends(const SeqView& s) {
+  const int32_t* p = s.cu ? s.cu : s.lengths;
+  return {p[0], p[s.cu ? s.seqs : 0]};
+}
+
+LTC_HD Unnamed unnamed_rows(const SeqView& s, const Ends& e) {
+  const uint32_t before = s.cu ? clip_rows(e.first, s.rows) : 0, end = s.cu ? clip_rows(e.last, s.rows) : s.rows;
+  const uint32_t behind = end > before ? end : before;
+  return {before, behind, before + (s.rows - behind)};
+}
+
+LTC_HD uint32_t unnamed_row(const Unnamed& u, uint32_t i) { return i < u.before ? i : u.behind + (i - u.before); }
+
 // Workgroups are numbered so that a workgroup finds its sequence without
 // knowing any count but the rows and sequences of the call: sequence i's
 // units begin at first(i) = clip(cu[i]) * mul / div + extra * i, a
@@ -137,7 +162,7 @@ LTC_HD bool locate_unit(const CacheView& c, const SeqView& s, const UnitMap& m, 
                         uint32_t* seq, Span* sp, uint64_t* own) {
   *seq = find_sequence(s.seqs, count);
   *sp = load_span(c, s, *seq);
-  const uint64_t first = unit_first(m, s, *seq);
+  const uint64_t first = unit_first(m, sp->row0, *seq);
   *own = unit - first;
   return sp->n != 0 && unit >= first;
 }

@@ -93,6 +93,15 @@ struct WaveCount {
   }
 };
 
+// Zeros for the rows of no sequence: `numbers` (a multiple of 8) at out +
+// row * stride, by worker's workgroup of `workers`.
+__device__ __forceinline__ void clear_unnamed(const Unnamed& u, uint16_t* out, uint64_t stride, uint32_t numbers,
+                                              uint64_t worker, uint64_t workers) {
+  const uint32_t parts = numbers / 8;
+  for (uint64_t i = worker * blockDim.x + threadIdx.x; i < (uint64_t)u.n * parts; i += workers * blockDim.x)
+    *reinterpret_cast<uint4v*>(out + unnamed_row(u, (uint32_t)(i / parts)) * stride + i % parts * 8) = uint4v{0, 0, 0, 0};
+}
+
 __device__ __forceinline__ void report(const CacheView& c, uint32_t bit) { atomicOr(c.status, bit); }
 
 }  // namespace ltc

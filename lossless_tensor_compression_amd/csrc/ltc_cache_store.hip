@@ -198,7 +198,12 @@ __global__ __launch_bounds__(1024) void k_cache_read(CacheView c, SeqView s, Uni
   uint32_t seq;
   Span sp;
   uint64_t j64;
+  const Ends ends = load_ends(s);
   const bool mine = locate_unit(c, s, map, blockIdx.x, WaveCount{s, map, blockIdx.x}, &seq, &sp, &j64);
+  const Unnamed none = unnamed_rows(s, ends);
+  if (none.n)
+    for (uint16_t* out : {k, v})
+      clear_unnamed(none, out + blockIdx.y * D, (uint64_t)c.heads * D, D, blockIdx.x, gridDim.x);
   if (!sp.ok && threadIdx.x == 0) report(c, kCacheBadSeq);
   if (!mine) return;
   j64 += sp.start >> c.page_log;

@@ -15,7 +15,8 @@ cache; their calls on one stream run in the order in which they are made.
 
 Rows cu[i]..cu[i+1] of a call belong to sequence i and stand for its last
 positions, lengths[i] - (cu[i+1] - cu[i]) to lengths[i] - 1; without cu each
-sequence has one row.  Position t of sequence i is token t % page of page
+sequence has one row.  Rows outside cu[0]..cu[-1] belong to no sequence and
+come out as zeros.  Position t of sequence i is token t % page of page
 table[i, t // page].  table, lengths and cu are int32 tensors on the GPU.
 """
 import ctypes
