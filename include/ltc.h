@@ -476,6 +476,8 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
  * LTC_CACHE_BAD_PAGE and LTC_CACHE_BAD_SEQUENCE in *d_status and touch nothing
  * out of bounds: such a page is not written, reads as zeros and is not
  * attended to; such a sequence is not written, and its rows get zeros.
+ * Where offsets decrease, other sequences lay claim to its rows or are passed
+ * over: what the call's rows get is then not defined, only that it is reported.
  * The status is only ever added to; a caller clears it when it has read it.
  *
  * Argument errors that the host sees (types, sizes, null or misaligned

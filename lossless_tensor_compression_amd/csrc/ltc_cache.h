@@ -59,31 +59,6 @@ LTC_HD Span span_of(int32_t c0, int32_t c1, int32_t length, uint32_t rows, uint6
   return s;
 }
 
-// Rows of the call that belong to no sequence, [0, before) and [behind, rows):
-// a call of a fixed number of rows may have fewer sequences' rows in it.
-struct Unnamed {
-  uint32_t before, behind, n;
-};
-
-// The row offsets that say so, to be loaded early (without branches: they come
-// with other loads).
-struct Ends {
-  int32_t first, last;
-};
-
-LTC_HD Ends load_ends(const SeqView& s) {
-  const int32_t* p = s.cu ? s.cu : s.lengths;
-  return {p[0], p[s.cu ? s.seqs : 0]};
-}
-
-LTC_HD Unnamed unnamed_rows(const SeqView& s, const Ends& e) {
-  const uint32_t before = s.cu ? clip_rows(e.first, s.rows) : 0, end = s.cu ? clip_rows(e.last, s.rows) : s.rows;
-  const uint32_t behind = end > before ? end : before;
-  return {before, behind, before + (s.rows - behind)};
-}
-
-LTC_HD uint32_t unnamed_row(const Unnamed& u, uint32_t i) { return i < u.before ? i : u.behind + (i - u.before); }
-
 // Workgroups are numbered so that a workgroup finds its sequence without
 // knowing any count but the rows and sequences of the call: sequence i's
 // units begin at first(i) = clip(cu[i]) * mul / div + extra * i, a
@@ -144,11 +119,51 @@ LTC_HD uint32_t find_sequence(uint32_t seqs, Count count) {
 // 32 bits.
 constexpr uint64_t kMaxPositions = 1u << 30;
 
+LTC_HD uint64_t capacity_of(const CacheView& c, const SeqView& s) {
+  const uint64_t capacity = (uint64_t)s.width << c.page_log;
+  return capacity < kMaxPositions ? capacity : kMaxPositions;
+}
+
 LTC_HD Span load_span(const CacheView& c, const SeqView& s, uint32_t seq) {
   const int32_t c0 = s.cu ? s.cu[seq] : (int32_t)seq, c1 = s.cu ? s.cu[seq + 1] : (int32_t)seq + 1;
-  const uint64_t capacity = (uint64_t)s.width << c.page_log;
-  return span_of(c0, c1, s.lengths[seq], s.rows, capacity < kMaxPositions ? capacity : kMaxPositions);
+  return span_of(c0, c1, s.lengths[seq], s.rows, capacity_of(c, s));
 }
+
+// What a unit loads besides its own sequence's numbers, early and without
+// branches, so that it comes with other loads: the ends of the row offsets, and
+// the numbers of the sequence that it checks (check_sequence).
+struct Early {
+  int32_t first, last;
+  int32_t c0, c1, length;
+};
+
+LTC_HD Early load_early(const SeqView& s, uint64_t unit) {
+  const uint32_t i = unit < s.seqs ? (uint32_t)unit : s.seqs - 1;
+  const int32_t* p = s.cu ? s.cu : s.lengths;
+  const uint32_t end = s.cu ? s.seqs : 0, c0 = s.cu ? i : 0, c1 = s.cu ? i + 1 : 0;
+  return {p[0], p[end], p[c0], p[c1], s.lengths[i]};
+}
+
+// Whether the sequence of the unit's own number is in order.  A search over row
+// offsets that decrease may pass by the sequence at fault, and a call has at
+// least as many units as sequences: so all are checked.
+LTC_HD bool check_sequence(const CacheView& c, const SeqView& s, const Early& e) {
+  return !s.cu || span_of(e.c0, e.c1, e.length, s.rows, capacity_of(c, s)).ok;
+}
+
+// Rows of the call that belong to no sequence, [0, before) and [behind, rows):
+// a call of a fixed number of rows may have fewer sequences' rows in it.
+struct Unnamed {
+  uint32_t before, behind, n;
+};
+
+LTC_HD Unnamed unnamed_rows(const SeqView& s, const Early& e) {
+  const uint32_t before = s.cu ? clip_rows(e.first, s.rows) : 0, end = s.cu ? clip_rows(e.last, s.rows) : s.rows;
+  const uint32_t behind = end > before ? end : before;
+  return {before, behind, before + (s.rows - behind)};
+}
+
+LTC_HD uint32_t unnamed_row(const Unnamed& u, uint32_t i) { return i < u.before ? i : u.behind + (i - u.before); }
 
 LTC_HD uint64_t unit_first(const UnitMap& m, const SeqView& s, uint32_t seq) {
   return unit_first(m, s.cu ? clip_rows(s.cu[seq], s.rows) : seq, seq);

@@ -320,13 +320,13 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   uint32_t seq;
   Span sp;
   uint64_t own;
-  const Ends ends = load_ends(s);
+  const Early early = load_early(s, unit);
   const bool mine = locate_unit(c, s, map, unit, WaveCount{s, map, unit}, &seq, &sp, &own);
-  const Unnamed none = unnamed_rows(s, ends);
+  const Unnamed none = unnamed_rows(s, early);
   if (none.n)
     clear_unnamed(none, a.out + (uint64_t)head * G * D, (uint64_t)a.q_heads * D, G * D, (uint64_t)unit * splits + split,
                   (uint64_t)units * splits);
-  if (!sp.ok && threadIdx.x == 0) report(c, kCacheBadSeq);
+  if (!(sp.ok && check_sequence(c, s, early)) && threadIdx.x == 0) report(c, kCacheBadSeq);
   const uint32_t packed = sp.n * G;
   if (!mine || own * R >= packed) return;
   const uint32_t r0 = (uint32_t)own * R, r1 = min(r0 + R, packed);
@@ -643,11 +643,11 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
   uint32_t seq;
   Span sp;
   uint64_t own;
-  const Ends ends = load_ends(s);
+  const Early early = load_early(s, unit);
   const bool mine = locate_unit(c, s, map, unit, WaveCount{s, map, unit}, &seq, &sp, &own);
-  const Unnamed none = unnamed_rows(s, ends);
+  const Unnamed none = unnamed_rows(s, early);
   if (none.n) clear_unnamed(none, a.out + (uint64_t)head * G * D, (uint64_t)a.q_heads * D, G * D, unit, units);
-  if (!sp.ok && threadIdx.x == 0) report(c, kCacheBadSeq);
+  if (!(sp.ok && check_sequence(c, s, early)) && threadIdx.x == 0) report(c, kCacheBadSeq);
   const uint32_t packed = sp.n * G;
   if (!mine || own * R >= packed) return;
   const uint32_t r0 = (uint32_t)own * R, r1 = min(r0 + R, packed);

@@ -54,8 +54,9 @@ __global__ __launch_bounds__(1024) void k_cache_write(CacheView c, SeqView s, Un
   uint32_t seq;
   Span sp;
   uint64_t j64;
+  const Early early = load_early(s, blockIdx.x);
   const bool mine = locate_unit(c, s, map, blockIdx.x, WaveCount{s, map, blockIdx.x}, &seq, &sp, &j64);
-  if (!sp.ok && threadIdx.x == 0) report(c, kCacheBadSeq);
+  if (!(sp.ok && check_sequence(c, s, early)) && threadIdx.x == 0) report(c, kCacheBadSeq);
   if (!mine || !sp.ok) return;
   j64 += sp.start >> c.page_log;
   if (j64 > ((sp.len - 1) >> c.page_log)) return;
@@ -198,13 +199,13 @@ __global__ __launch_bounds__(1024) void k_cache_read(CacheView c, SeqView s, Uni
   uint32_t seq;
   Span sp;
   uint64_t j64;
-  const Ends ends = load_ends(s);
+  const Early early = load_early(s, blockIdx.x);
   const bool mine = locate_unit(c, s, map, blockIdx.x, WaveCount{s, map, blockIdx.x}, &seq, &sp, &j64);
-  const Unnamed none = unnamed_rows(s, ends);
+  const Unnamed none = unnamed_rows(s, early);
   if (none.n)
     for (uint16_t* out : {k, v})
       clear_unnamed(none, out + blockIdx.y * D, (uint64_t)c.heads * D, D, blockIdx.x, gridDim.x);
-  if (!sp.ok && threadIdx.x == 0) report(c, kCacheBadSeq);
+  if (!(sp.ok && check_sequence(c, s, early)) && threadIdx.x == 0) report(c, kCacheBadSeq);
   if (!mine) return;
   j64 += sp.start >> c.page_log;
   // a refused sequence has start 0 here: its rows get zeros
