@@ -218,6 +218,8 @@ def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None):
     if _current_gpu() != cache._index:
         with torch.cuda.device(cache._index):
             return cache_attend(cache, q, table, lengths, cu, window, scale)
+    if not 0 <= window < 1 << 31:  # ctypes would take it modulo 2^32
+        raise LTCError(-1, f"window {window}")
     q, qr, (rows, q_heads, dim) = cache._rows(q, None, "q")
     s = cache._seqs(table, lengths, cu, rows)
     out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)

@@ -1,0 +1,26 @@
+"""Arguments that the key/value cache's binding refuses by itself, without a
+GPU."""
+import pytest
+import torch
+
+from cache_cpu import cpu_cache, sequences
+from lossless_tensor_compression_amd import LTCError
+from lossless_tensor_compression_amd import kv_cache as kc
+
+
+@pytest.mark.parametrize("window", [-1, -2 ** 31, -2 ** 32 + 5, 1 << 31, 2 ** 32, 2 ** 32 + 5, 2 ** 64 + 1])
+def test_windows_out_of_range(monkeypatch, window):
+    """Not taken modulo 2^32: a window of 2^32 + 5 is not one of 5."""
+    reached = []
+    cache = cpu_cache(monkeypatch, ltc_cache_attend=lambda *a: reached.append(a) or 0)
+    with pytest.raises(LTCError) as e:
+        kc.cache_attend(cache, torch.zeros((1, 4, 64), dtype=torch.bfloat16), *sequences([9]), window=window)
+    assert e.value.code == -1 and not reached
+
+
+@pytest.mark.parametrize("window", [0, 1, 2 ** 31 - 1])
+def test_windows_in_range(monkeypatch, window):
+    reached = []
+    cache = cpu_cache(monkeypatch, ltc_cache_attend=lambda *a: reached.append(a[4]) or 0)
+    kc.cache_attend(cache, torch.zeros((1, 4, 64), dtype=torch.bfloat16), *sequences([9]), window=window)
+    assert reached == [window]
