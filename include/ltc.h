@@ -535,17 +535,17 @@ int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k
  * reads head h / (q_heads / heads).  d_out [rows][q_heads][dim] (16-byte
  * aligned) gets softmax(scale * q k^T) v, zeros for a row that sees nothing.
  * (rows + seqs) * q_heads may be 2^31 at most.  A NaN among the keys or
- * values that a row sees makes it NaN (a value's, in its dim alone); what it
- * does not see has no part in it.  Weights are rounded to fp16 before they
- * meet the values, with 11 bits down to 2^-23 of the largest weight times
- * its page's value scale (below 2^-34 of it they are lost); sums are held in
- * fp32.  A result depends on the call's shapes, not on timing.  The
- * workspace has ltc_cache_attend_workspace_size() bytes, 256-byte aligned
- * (none may be needed, then d_ws may be NULL).  Its first LTC_CACHE_WS_ZEROS
- * bytes must be zero before the first call that uses it, and every call
- * leaves them zero: a caller clears a workspace once and keeps it.  Calls
- * that may run at the same
- * time need workspaces of their own. */
+ * values that a row sees makes it NaN (a value's, in its dim alone), and so
+ * does a NaN or an infinity in its query; what it does not see has no part
+ * in it.  Weights are rounded to fp16 before they meet the values, with 11
+ * bits down to 2^-23 of the largest weight times its page's value scale
+ * (below 2^-34 of it they are lost); sums are held in fp32.  A result
+ * depends on the call's shapes, not on timing.  The workspace has
+ * ltc_cache_attend_workspace_size() bytes, 256-byte aligned (none may be
+ * needed, then d_ws may be NULL).  Its first LTC_CACHE_WS_ZEROS bytes must
+ * be zero before the first call that uses it, and every call leaves them
+ * zero: a caller clears a workspace once and keeps it.  Calls that may run
+ * at the same time need workspaces of their own. */
 enum { LTC_CACHE_WS_ZEROS = 65536 };
 uint64_t ltc_cache_attend_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,
                                          uint32_t window);

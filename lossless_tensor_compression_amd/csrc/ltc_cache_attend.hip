@@ -280,6 +280,25 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Span& sp, u
   *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = out;
 }
 
+// A denominator of 0 is a row that sees nothing, and keeps its zeros, or one
+// whose scores are all -infinity, as an infinity in its query can make them:
+// that becomes NaN.  zero: the lane's row r is one; after its zeros are stored.
+template <int D>
+__device__ __forceinline__ void spoil_rows(const CacheView& c, const AttendArgs& a, const Span& sp, const int32_t* table,
+                                           uint32_t head, uint32_t G, uint32_t r, bool zero) {
+  const int lane = threadIdx.x & 63;
+  for (uint64_t left = __ballot(zero && sp.ok); left; left &= left - 1) {
+    const uint32_t row = __shfl(r, __builtin_ctzll(left)), token = row / G;
+    const uint32_t at = sp.start + token, last = at >> c.page_log;
+    const uint32_t first = (a.window && at >= a.window ? at + 1 - a.window : 0) >> c.page_log;
+    bool seen = false;
+    for (uint32_t j = first + lane; j <= last; j += 64) seen |= (uint32_t)table[j] < c.pages;
+    if (!__any(seen)) continue;
+    uint16_t* out = a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + head * G + row % G) * D;
+    for (int d = lane * 2; d < D; d += 128) *reinterpret_cast<uint32_t*>(out + d) = 0x7fff7fffu;  // NaN in both types
+  }
+}
+
 // Waves for each SIMD that the kernel's registers are to leave room for: as many
 // as they do without spills.  3 instead of 2 for one column block of 128 dims:
 // 64 rows at 1,000-6,000 positions 93 -> 107 us, one at 131,071 57 -> 61 us; 2
@@ -507,7 +526,14 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     }
     __syncthreads();
   }
-  if (rg.used <= 1) return;
+  if (rg.used <= 1) {
+    if (wave == 0) {
+      bool zero = lane < R && r0 + lane < packed;
+      for (int v = 0; v < W; ++v) zero = zero && lds_m[v][lane % R] == -INFINITY && lds_l[v][lane % R] == 0.0f;
+      spoil_rows<D>(c, a, sp, table, head, G, r0 + lane, zero);
+    }
+    return;
+  }
 
   // ---- the splits' parts together, by the workgroup that comes last (and in
   // the splits' order, so that the order of coming does not matter).  One
@@ -566,6 +592,15 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   };
   const int parts = max(GROUPS / live, 1), mine_of = grp % parts;
   float* lds_flat = &lds_acc[0][0][0];
+  // all waves ask the same, since the answer holds a barrier
+  auto spoil = [&] {
+    const bool none = lane < live && lds_m[0][lane % R] == -INFINITY;
+    if (!__any(none)) return;
+    bool zero = none;
+    for (int i = 0; i < rg.used; ++i) zero = zero && get2(part_ml + (at0 + (uint64_t)i * R + lane % R) * 2)[1] == 0.0f;
+    __syncthreads();
+    if (wave == 0) spoil_rows<D>(c, a, sp, table, head, G, r0 + lane, zero);
+  };
   if (parts == 1) {
     constexpr int RA = 4;
     for (int r = grp; r < live && grp < GROUPS; r += RA * GROUPS) {
@@ -575,6 +610,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
       for (int k = 0; k < RA; ++k)
         if (r + k * GROUPS < live) store_row<D>(a, sp, head, G, bf16, r0 + r + k * GROUPS, x * 4, sum[k], below[k]);
     }
+    spoil();
     return;
   }
   const int row = grp / parts;
@@ -586,14 +622,16 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     if (x == 0) lds_l[0][grp] = below[0];
   }
   __syncthreads();
-  if (mine_of != 0 || row >= live || grp >= GROUPS) return;
-  float4v sum = {0, 0, 0, 0};
-  float below = 0.0f;
-  for (int i = 0; i < parts; ++i) {
-    sum += *reinterpret_cast<const float4v*>(lds_flat + ((grp + i) * LANES + x) * 4);
-    below += lds_l[0][grp + i];
+  if (mine_of == 0 && row < live && grp < GROUPS) {
+    float4v sum = {0, 0, 0, 0};
+    float below = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+      sum += *reinterpret_cast<const float4v*>(lds_flat + ((grp + i) * LANES + x) * 4);
+      below += lds_l[0][grp + i];
+    }
+    store_row<D>(a, sp, head, G, bf16, r0 + row, x * 4, sum, below);
   }
-  store_row<D>(a, sp, head, G, bf16, r0 + row, x * 4, sum, below);
+  spoil();
 }
 
 constexpr uint32_t kTileRows = 128;
@@ -795,6 +833,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
     const uint32_t r = w0 + nc * 16 + n;
     if (r < packed)
       for (int i = 0; i < DB; ++i) store_row<D>(a, sp, head, G, bf16, r, i * 16 + 4 * g, w.acc[nc][i], below);
+    spoil_rows<D>(c, a, sp, table, head, G, r, g == 0 && r < packed && below == 0.0f);
   }
 }
 
