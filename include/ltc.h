@@ -539,8 +539,9 @@ int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k
  * does a NaN or an infinity in its query; what it does not see has no part
  * in it.  Weights are rounded to fp16 before they meet the values, with 11
  * bits down to 2^-23 of the largest weight times its page's value scale
- * (below 2^-34 of it they are lost); sums are held in fp32.  A result
- * depends on the call's shapes, not on timing.  The workspace has
+ * (below 2^-34 of it they are lost); scores and sums are held in fp32, and
+ * |scale * q k| is to stay below 2^25 (past it weights lose all their bits).
+ * A result depends on the call's shapes, not on timing.  The workspace has
  * ltc_cache_attend_workspace_size() bytes, 256-byte aligned (none may be
  * needed, then d_ws may be NULL).  Its first LTC_CACHE_WS_ZEROS bytes must
  * be zero before the first call that uses it, and every call leaves them

@@ -22,6 +22,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A step whose largest x + w is within kSlack of the running bound keeps the
 // bound, so the accumulators are seldom scaled.
 constexpr int kSlack = 6;
+// Far from zero the bound and the sums with it are rounded to steps of 2^-23 of
+// it: it is put four to eight steps higher, so that no weight passes fp16's top.
+// Past 2^26 that takes all of a weight's bits.
+constexpr float kFar = 0x1p-21f;
 // Weights meet the codes times 2^kHead, which puts the largest at 2^15, below
 // fp16's top.  A position that takes nearly all of the weight may have values
 // near zero, and then the output is what thousands of far smaller weights make
@@ -199,10 +203,10 @@ __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4
     for (int b = 0; b < 4; ++b)
       for (int i = 0; i < 4; ++i) top = fmaxf(top, st[nc][b][i]);
     top = fmaf(top, f, wv);
-    if (__any(top > w.m[nc] + kSlack)) {
+    if (__any(top > fmaf(fabsf(w.m[nc]), -kFar, w.m[nc]) + kSlack)) {
       float now = fmaxf(top, __shfl_xor(top, 16));
       now = fmaxf(now, __shfl_xor(now, 32));
-      now = fmaxf(now, w.m[nc]);
+      now = fmaxf(fmaf(fabsf(now), kFar, now), w.m[nc]);  // -infinity: NaN, and the maximum is the other
       const float keep = now == w.m[nc] ? 1.0f : __builtin_amdgcn_exp2f(w.m[nc] - now);
       w.l[nc] = rebase(w.l[nc], w.m[nc], now);
       w.m[nc] = now;
