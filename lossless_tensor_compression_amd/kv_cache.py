@@ -10,7 +10,8 @@ A binding over ltc_cache_write, ltc_cache_read and ltc_cache_attend of
 include/ltc.h, where the layouts, the rounding and what happens with bad
 tables are written down.  Calls run on the current stream, allocate nothing
 but their outputs and a workspace that the cache keeps for each stream, and
-never synchronise, so they can be captured in a graph.  Threads may share a
+never synchronise, so they can be captured in a graph.  They have no backward
+pass: rows that require a gradient are refused.  Threads may share a
 cache; their calls on one stream run in the order in which they are made.
 
 Rows cu[i]..cu[i+1] of a call belong to sequence i and stand for its last
@@ -166,6 +167,8 @@ class KVCache:
         alignment do not let them), its ltc_cache_rows as bytes and its shape."""
         if t.dtype is not self.dtype or t.get_device() != self._index:
             raise ValueError(f"{name} must be {self.dtype} on the cache's GPU")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, which the cache's operators have not: call under torch.no_grad()")
         shape = t.shape
         if len(shape) != 3 or shape[2] != self.dim or (heads is not None and shape[1] != heads):
             raise ValueError(f"{name} must be [rows, {'heads' if heads is None else heads}, {self.dim}]")

@@ -24,3 +24,25 @@ def test_windows_in_range(monkeypatch, window):
     cache = cpu_cache(monkeypatch, ltc_cache_attend=lambda *a: reached.append(a[4]) or 0)
     kc.cache_attend(cache, torch.zeros((1, 4, 64), dtype=torch.bfloat16), *sequences([9]), window=window)
     assert reached == [window]
+
+
+def test_rows_that_require_a_gradient(monkeypatch):
+    """An output without one would be detached silently."""
+    reached = []
+    cache = cpu_cache(monkeypatch, **{n: lambda *a: reached.append(a) or 0 for n in ("ltc_cache_attend", "ltc_cache_write")})
+    x = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    w = torch.ones((), dtype=torch.bfloat16, requires_grad=True)
+    for leaf in (x.clone().requires_grad_(), x * w):
+        with pytest.raises(ValueError, match="gradient"):
+            kc.cache_attend(cache, leaf, *sequences([9]))
+        for k, v in ((leaf, x), (x, leaf)):
+            with pytest.raises(ValueError, match="gradient"):
+                kc.cache_write(cache, k, v, *sequences([9]))
+        assert not reached
+        with torch.no_grad():
+            kc.cache_attend(cache, leaf, *sequences([9]))
+            kc.cache_write(cache, leaf, leaf, *sequences([9]))
+        assert len(reached) == 2
+        reached.clear()
+        kc.cache_attend(cache, leaf.detach(), *sequences([9]))
+        reached.clear()
