@@ -303,10 +303,14 @@ __device__ __forceinline__ void spoil_rows(const CacheView& c, const AttendArgs&
   }
 }
 
-// Waves for each SIMD that the kernel's registers are to leave room for: as many
-// as they do without spills.  3 instead of 2 for one column block of 128 dims:
-// 64 rows at 1,000-6,000 positions 93 -> 107 us, one at 131,071 57 -> 61 us; 2
-// instead of 1 for 192 dims: 170 -> 207 us.
+// Waves for each SIMD that the kernel's registers are to leave room for.  3
+// instead of 2 for one column block of 64 dims, where the join of the splits then
+// spills 32 registers (the loop none): 23 rows with a window of 1,024 18.7 -> 16.1
+// us, 64 rows at 1,000-6,000 positions of 16 heads 109 -> 102 us, 200 at 10-900
+// 32 -> 26 us.  3 instead of 2 for one of 128 dims: 64 rows at 1,000-6,000 93 -> 107
+// us, one at 131,071 57 -> 61 us; 2 instead of 1 for 192 dims: 170 -> 207 us.  The
+// most that go without spills else, but for 3 registers of E4M3's two blocks of
+// 128 dims.
 constexpr int rows_occupancy(int D, int NC) { return D * NC <= 64 ? 3 : D * NC <= 256 && D < 192 ? 2 : 1; }
 
 // W waves on a tile of 16 * NC packed rows (row r of a sequence and key head
@@ -326,7 +330,7 @@ constexpr int rows_occupancy(int D, int NC) { return D * NC <= 64 ? 3 : D * NC <
 // step's are used up, and so for values, so one step (2 * 64 * D bytes) is in
 // flight for each wave.  Bound by memory where there is enough to read: 64 rows
 // at 1,001-6,001 positions (8 heads of 128, 32 query heads) 93 us, 4.6 TB/s, one
-// at 131,071 57.5 us; by the chain lengths, table, codes, partial results, join
+// at 131,071 58 us; by the chain lengths, table, codes, partial results, join
 // where there is not: one at 777 positions 9 us.
 template <bool E4M3, int D, int NC, int W>
 __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
@@ -641,7 +645,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
 constexpr uint32_t kTileRows = 128;
 // Workgroups on a CU: as many as registers and shared memory hold.  3 instead
 // of 2 for one prompt of 4,096 rows of 64 dims: 142 -> 115 us; for 2,048 rows of
-// 96 dims registers spill: 64 -> 94 us.
+// 96 dims registers spill: 64 -> 94 us (for E4M3's 64 dims one does).
 constexpr int tiles_occupancy(int D) { return D <= 64 ? 3 : D <= 128 ? 2 : 1; }
 
 // The order of a run of 4 * N reads of shared memory and their 4 * N * NC
@@ -662,7 +666,7 @@ template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
 // lanes take them, so that every access is one run of 1 KB: while a step is
 // computed the next one's are turned, and those of the one behind it are on
 // their way from memory.  Eight prompts of 4,096 rows behind 4,096 positions (8
-// heads of 128, 32 query heads) 3.6 ms, 915 TFLOP/s, where k_attend_rows takes
+// heads of 128, 32 query heads) 3.64 ms, 906 TFLOP/s, where k_attend_rows takes
 // 4.2 ms: a library product of 8,192 reaches 1,250.  Matrix cores are busy for
 // 35% of the time, vector units for 60%; without exp2 it is as fast, without
 // turning 12% faster, without loads 14%, with an eighth of the second product

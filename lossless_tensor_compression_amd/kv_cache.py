@@ -217,7 +217,9 @@ def cache_read(cache, table, lengths, cu=None, rows=None):
 def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None):
     """softmax(scale * q k^T) v of queries [rows, q_heads, dim] over the
     positions up to each row's own (with window: the last `window` of them);
-    zeros for a row that sees nothing.  scale is dim^-0.5 by default."""
+    zeros for a row that sees nothing.  scale is dim^-0.5 by default.  A call
+    is planned for sequences of about its mean: a prompt, or a context of many
+    times the others' length, is faster in a call of its own."""
     if _current_gpu() != cache._index:
         with torch.cuda.device(cache._index):
             return cache_attend(cache, q, table, lengths, cu, window, scale)
