@@ -483,7 +483,7 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
  * Argument errors that the host sees (types, sizes, null or misaligned
  * pointers, more than 2^24 rows or 2^20 sequences) return before anything is
  * enqueued.  A call without rows or sequences succeeds and does nothing. */
-enum { LTC_E4M3 = 0, LTC_INT8 = 1 };
+enum { LTC_E4M3 = 0, LTC_INT8 = 1, LTC_E2M1 = 3 };
 enum { LTC_CACHE_BAD_PAGE = 1, LTC_CACHE_BAD_SEQUENCE = 2 };
 
 typedef struct {

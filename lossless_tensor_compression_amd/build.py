@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libltc.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["ltc_compress.hip", "ltc_decompress.hip", "ltc_crc32.hip", "ltc_api.hip",
-           "ltc_cache_store.hip", "ltc_cache_attend.hip", "ltc_cache_api.hip"]
+           "ltc_cache_store.hip", "ltc_cache_store4.hip", "ltc_cache_attend.hip", "ltc_cache_attend_int8.hip",
+           "ltc_cache_attend_e2m1.hip", "ltc_cache_api.hip"]
 # plain C++ (no device code): the host-side parsing of blob bytes
 HOST_SOURCES = ["ltc_host.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,4 +1,4 @@
-// ltc_cache.h -- the paged 8-bit key/value cache: what a kernel is given, and
+// ltc_cache.h -- the paged key/value cache: what a kernel is given, and
 // the index arithmetic that turns a workgroup's number into a sequence, its
 // rows and the pages under them.  Everything here runs on the host too, so
 // that it can be checked there against bad tables, lengths and row offsets.
@@ -19,9 +19,9 @@ constexpr uint32_t kCacheBadPage = 1;  // a table entry outside [0, pages)
 constexpr uint32_t kCacheBadSeq = 2;   // lengths or row offsets that contradict each other
 
 struct CacheView {
-  uint8_t* k;        // [pages][heads][page/16][dim/16][16 tokens][16 dims]
+  uint8_t* k;        // [pages][heads][page/16][dim/16][16 tokens][16 dims]; of 4 bits [dim/32][16 tokens][32 dims]
   uint8_t* v;        // [pages][heads][page/16][dim][16 tokens]
-  uint8_t* scales;   // [pages][heads][2], 2^(byte - 127)
+  uint8_t* scales;   // [pages][heads][2], 2^(byte - 127); of 4 bits see token_scales
   uint32_t* status;  // one word, bits above
   uint32_t pages, heads, dim;
   uint32_t page_log;  // log2 of a page's tokens
@@ -188,6 +188,16 @@ LTC_HD uint64_t head_offset(const CacheView& c, uint32_t page, uint32_t head) {
   return (((uint64_t)page * c.heads + head) * c.dim) << c.page_log;
 }
 
+// A cache of 4-bit codes: half of head_offset's bytes, and for each page and head
+// the exponents of the tokens' keys, those of their values (a byte each, 2^(byte -
+// 127)), and drop_bytes for each token: nibble j, the lowest first, is how far
+// below the token's the exponent of its key's dims 32 j .. 32 j + 31 lies.
+constexpr int kMostDrop = 15;
+LTC_HD constexpr uint32_t drop_bytes(uint32_t dim) { return dim <= 64 ? 1 : dim <= 128 ? 2 : 4; }
+LTC_HD uint64_t token_scales(const CacheView& c, uint32_t page, uint32_t head) {
+  return (((uint64_t)page * c.heads + head) * (2 + drop_bytes(c.dim))) << c.page_log;
+}
+
 // Within a page and head: the code of token t (0 <= t < page) and dim d.
 LTC_HD uint32_t k_code(uint32_t t, uint32_t d, uint32_t dim) {
   return (t >> 4) * 16 * dim + (d >> 4) * 256 + (t & 15) * 16 + (d & 15);
@@ -229,6 +239,18 @@ LTC_HD uint32_t scale_byte(float largest, bool e4m3) {
   const int e = (int)(x.u >> 23) - 126;  // largest = 0.5..1 times 2^e; subnormal: far below the lowest
   const int s = e4m3 ? (mantissa <= 0x600000 ? e - 9 : e - 8) : (mantissa <= 0x7e0000 ? e - 7 : e - 6);
   return (uint32_t)((s < kLowestScale ? kLowestScale : s) + 127);
+}
+
+// The least e with largest <= 6 * 2^e = 0.75 * 2^(e + 3), the top of E2M1's codes;
+// of 0 one that is below all others.
+LTC_HD int e2m1_exponent(float largest) {
+  union {
+    float f;
+    uint32_t u;
+  } x;
+  x.f = largest;
+  const int e = (int)(x.u >> 23) - 126;
+  return (x.u & 0x7fffff) <= 0x400000 ? e - 3 : e - 2;
 }
 
 }  // namespace ltc

@@ -19,13 +19,14 @@ bool aligned(const void* p, uintptr_t to) { return p && reinterpret_cast<uintptr
 int check_cache(const ltc_cache* c, CacheView* out) {
   if (!c) return LTC_ERR_INVALID_ARGUMENT;
   if (c->dtype != LTC_BF16 && c->dtype != LTC_FP16) return LTC_ERR_UNSUPPORTED_DTYPE;
-  if (c->codes != LTC_E4M3 && c->codes != LTC_INT8) return LTC_ERR_UNSUPPORTED_DTYPE;
+  if (c->codes != LTC_E4M3 && c->codes != LTC_INT8 && c->codes != LTC_E2M1) return LTC_ERR_UNSUPPORTED_DTYPE;
   if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return LTC_ERR_INVALID_ARGUMENT;
   if (c->dim != 64 && c->dim != 96 && c->dim != 128 && c->dim != 192 && c->dim != 256)
     return LTC_ERR_INVALID_ARGUMENT;
   if (c->heads < 1 || c->heads > kMaxHeads || c->pages > kMaxPages) return LTC_ERR_INVALID_ARGUMENT;
   if (!aligned(c->d_status, 4)) return LTC_ERR_INVALID_ARGUMENT;
-  if (c->pages && (!aligned(c->d_k_codes, 16) || !aligned(c->d_v_codes, 16) || !aligned(c->d_scales, 2)))
+  if (c->pages && (!aligned(c->d_k_codes, 16) || !aligned(c->d_v_codes, 16) ||
+                   !aligned(c->d_scales, c->codes == LTC_E2M1 ? 16 : 2)))
     return LTC_ERR_INVALID_ARGUMENT;
   out->k = static_cast<uint8_t*>(c->d_k_codes);
   out->v = static_cast<uint8_t*>(c->d_v_codes);
@@ -91,6 +92,7 @@ int ltc_cache_write(const ltc_cache* cache, const ltc_cache_seqs* seqs, const lt
   if (!rc) rc = check_rows(k, &kr);
   if (!rc) rc = check_rows(v, &vr);
   if (rc) return rc;
+  if (cache->codes == LTC_E2M1) return launched(launch_cache4_write(c, s, cache->dtype, kr, vr, stream));
   return launched(launch_cache_write(c, s, cache->codes == LTC_E4M3, cache->dtype, kr, vr, stream));
 }
 
@@ -101,8 +103,9 @@ int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k
   if (!rc) rc = check_seqs(seqs, &s);
   if (rc || !s.rows) return rc;
   if (!aligned(d_k, 16) || !aligned(d_v, 16)) return LTC_ERR_INVALID_ARGUMENT;
-  return launched(launch_cache_read(c, s, cache->codes == LTC_E4M3, cache->dtype, static_cast<uint16_t*>(d_k),
-                                    static_cast<uint16_t*>(d_v), stream));
+  uint16_t *k = static_cast<uint16_t*>(d_k), *v = static_cast<uint16_t*>(d_v);
+  if (cache->codes == LTC_E2M1) return launched(launch_cache4_read(c, s, cache->dtype, k, v, stream));
+  return launched(launch_cache_read(c, s, cache->codes == LTC_E4M3, cache->dtype, k, v, stream));
 }
 
 uint64_t ltc_cache_attend_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,
@@ -135,7 +138,8 @@ int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const l
   a.window = window;
   a.scale = scale;
   a.ws = d_ws;
-  return launched(launch_cache_attend(c, s, cache->codes == LTC_E4M3, cache->dtype, a, stream));
+  a.lse = nullptr;
+  return launched(launch_cache_attend(c, s, cache->codes, cache->dtype, a, stream));
 }
 
 }  // extern "C"

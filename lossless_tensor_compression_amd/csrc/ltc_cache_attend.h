@@ -1,4 +1,5 @@
-// ltc_cache_attend.hip -- attention of new queries over the 8-bit cache.
+// ltc_cache_attend.h -- attention of new queries over the cache: the kernels, for
+// the file of each code type to build.
 //
 // One pass over the positions with the softmax's running maximum and sum.
 // Per head, with x_t = log2(e) scale (q . k_t) and 2^w the scale of token t's
@@ -9,7 +10,8 @@
 // below the fraction gathers u_t 2^-w: so the weights that multiply the codes
 // have one range whatever the pages' scales are, and the codes go into the
 // matrix cores as they are.  The matrix cores get 2^kHead u_t, rounded to fp16.
-#include <type_traits>
+// With 4-bit codes every token has scales of its own, and so w (step_weights4).
+#pragma once
 
 #include "ltc_cache_device.h"
 
@@ -36,13 +38,13 @@ constexpr int kHead = 15 - kSlack;
 
 // Eight codes (two dwords) as fp16, exactly: E4M3 has 3 bits of mantissa and
 // exponents down to 2^-9, INT8 7 bits.
-template <bool E4M3> __device__ __forceinline__ half8 codes_to_half(uint32_t a, uint32_t b) {
+template <int CODES> __device__ __forceinline__ half8 codes_to_half(uint32_t a, uint32_t b) {
   union {
     half8 h8;
     half2v h2[4];
     uint32_t u[4];
   } r;
-  if constexpr (E4M3) {
+  if constexpr (CODES == LTC_E4M3) {
     r.h2[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)a, 1.0f, false);
     r.h2[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)a, 1.0f, true);
     r.h2[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b, 1.0f, false);
@@ -60,6 +62,64 @@ template <bool E4M3> __device__ __forceinline__ half8 codes_to_half(uint32_t a, 
   }
   return r.h8;
 }
+
+// Eight E2M1 codes times scale as fp16.
+__device__ __forceinline__ half8 codes4_to_half(uint32_t c, float scale) {
+  union {
+    half8 h8;
+    half2v h2[4];
+  } r;
+  r.h2[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 0);
+  r.h2[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 1);
+  r.h2[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 2);
+  r.h2[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, 3);
+  return r.h8;
+}
+
+// Keys of 4-bit codes go into the products as codes times 2^(kLift - drop): with 15,
+// the most, 0.5 is 2^-6 then, a normal fp16 number, and with 0 the top is 6,144.
+constexpr int kLift = 10;
+
+// Which dims a lane's k-group g of a key's product x covers, eight from this one
+// on.  The lane's 16 bytes of keys are 16 dims of 8 bits, so two products, or 32 of
+// 4 bits, which share a scale: four; what is left of the dims goes in half and
+// quarter loads.
+template <int CODES, int D> __device__ __forceinline__ int dim_of(int x, int g) {
+  if constexpr (CODES == LTC_E2M1) {
+    constexpr int F = D / 128 * 4, H = D % 128 / 64 * 2;
+    return x < F ? x / 4 * 128 + g * 32 + x % 4 * 8 : x < F + H ? F * 32 + g * 16 + (x - F) * 8 : D - 32 + g * 8;
+  } else {
+    constexpr int KL = D / 64;
+    return x < 2 * KL ? (4 * (x / 2) + g) * 16 + (x & 1) * 8 : 64 * KL + g * 8;
+  }
+}
+
+// A token's keys in 4 bits as the lane takes them: dword x is those of product x.
+// at: the token's block of 32 dims 0.
+template <int D> struct Keys4 {
+  uint32_t c[D / 32];
+  uint32_t drops;
+  __device__ __forceinline__ void load(const uint8_t* at, const uint8_t* drops_at, int g) {
+    constexpr int F = D / 128;
+    for (int j = 0; j < F; ++j) {
+      const uint4v x = *reinterpret_cast<const uint4v*>(at + (4 * j + g) * 256);
+      for (int i = 0; i < 4; ++i) c[4 * j + i] = x[i];
+    }
+    if constexpr (D % 128 >= 64) {
+      const uint2v x = *reinterpret_cast<const uint2v*>(at + (4 * F + (g >> 1)) * 256 + (g & 1) * 8);
+      c[4 * F] = x[0];
+      c[4 * F + 1] = x[1];
+    }
+    if constexpr (D % 64) c[D / 32 - 1] = *reinterpret_cast<const uint32_t*>(at + (D / 32 - 1) * 256 + g * 4);
+    drops = load_drops<(int)drop_bytes(D)>(drops_at);
+  }
+  __device__ __forceinline__ half8 half(int x, int g) const {
+    constexpr int F = D / 128 * 4, H = D % 128 / 64 * 2;
+    const int block = x < F ? x / 4 * 4 + g : x < F + H ? F + (g >> 1) : D / 32 - 1;
+    const uint32_t drop = drops >> (4 * block) & 15;
+    return codes4_to_half(c[x], __builtin_bit_cast(float, ((uint32_t)(127 + kLift) - drop) << 23));
+  }
+};
 
 // Whether any of four E4M3 codes is a NaN (0x7f or 0xff).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
@@ -135,10 +195,10 @@ template <int D, int NC> struct Rows {
 };
 
 // Rows r0.. of a sequence and head; those from packed on are none, and see nothing.
-template <int D, int NC>
+template <int CODES, int D, int NC>
 __device__ __forceinline__ void load_rows(Rows<D, NC>& w, const AttendArgs& a, const Span& sp, uint32_t head, uint32_t G,
                                           uint32_t r0, uint32_t packed, bool bf16, int n, int g) {
-  constexpr int KS = D / 32, KL = D / 64;
+  constexpr int KS = D / 32;
   for (int nc = 0; nc < NC; ++nc) {
     const uint32_t r = r0 + nc * 16 + n;
     const bool live = r < packed;
@@ -148,8 +208,7 @@ __device__ __forceinline__ void load_rows(Rows<D, NC>& w, const AttendArgs& a, c
     w.lo[nc] = a.window ? max(w.hi[nc] - (int)a.window, 0) : 0;
     uint4v raw[KS];
     for (int x = 0; x < KS; ++x) {
-      const int d = x < 2 * KL ? (4 * (x / 2) + g) * 16 + (x & 1) * 8 : 64 * KL + g * 8;
-      raw[x] = live ? *reinterpret_cast<const uint4v*>(src + d) : uint4v{0, 0, 0, 0};
+      raw[x] = live ? *reinterpret_cast<const uint4v*>(src + dim_of<CODES, D>(x, g)) : uint4v{0, 0, 0, 0};
     }
     w.up[nc] = 0;
     if (bf16) {
@@ -235,6 +294,51 @@ __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4
   }
 }
 
+// The same for tokens that have scales of their own: ke and ve are the bytes of
+// the lane's 16 tokens' exponents, and the keys' codes came times 2^(kLift - drop).
+// Everything is 127 higher than x + w: the byte stands for w.
+template <int D, int NC>
+__device__ __forceinline__ void step_weights4(Rows<D, NC>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], float base,
+                                              uint4v ke, uint4v ve, int tv, bool edge, bool have) {
+  const float f = fmaxf(base * power_of_two(-kLift), 0x1p-126f);  // not 0: hidden scores are -infinity
+#pragma unroll
+  for (int nc = 0; nc < NC; ++nc) {
+    float top = -INFINITY;
+    for (int b = 0; b < 4; ++b)
+      for (int i = 0; i < 4; ++i) {
+        const float wv = (float)(ve[b] >> (8 * i) & 0xff);
+        float x = __builtin_amdgcn_ldexpf(st[nc][b][i], (int)(ke[b] >> (8 * i) & 0xff) - 127 - w.up[nc]) * f;
+        if (edge) {
+          const int t = tv + 4 * b + i;
+          const bool seen = t >= w.lo[nc] && t < w.hi[nc] && have;
+          x = seen ? x : -INFINITY;
+        }
+        st[nc][b][i] = x;
+        top = fmaxf(top, x + wv);
+      }
+    if (__any(top > fmaf(fabsf(w.m[nc]), -kFar, w.m[nc]) + kSlack)) {
+      float now = fmaxf(top, __shfl_xor(top, 16));
+      now = fmaxf(now, __shfl_xor(now, 32));
+      now = fmaxf(fmaf(fabsf(now), kFar, now), w.m[nc]);  // -infinity: NaN, and the maximum is the other
+      const float keep = now == w.m[nc] ? 1.0f : __builtin_amdgcn_exp2f(w.m[nc] - now);
+      w.l[nc] = rebase(w.l[nc], w.m[nc], now);
+      w.m[nc] = now;
+      for (int i = 0; i < D / 16; ++i) w.acc[nc][i] *= keep;
+    }
+    // nothing seen yet: every weight is 0
+    const float m = w.m[nc] == -INFINITY ? 0.0f : w.m[nc];
+    float sum = 0.0f;
+    for (int b = 0; b < 4; ++b)
+      for (int i = 0; i < 4; ++i) {
+        const float wv = (float)(ve[b] >> (8 * i) & 0xff);
+        p[nc][b >> 1][(b & 1) * 4 + i] = (_Float16)__builtin_amdgcn_exp2f(st[nc][b][i] + (wv - m + kHead));
+        // not the weight times 2^-w: that may be below fp32's numbers where this is not
+        sum += __builtin_amdgcn_exp2f(st[nc][b][i] + (127.0f - m));
+      }
+    w.l[nc] += sum;
+  }
+}
+
 // NaN among a step's value codes (the lane's 16 of dim 16 i + n are at
 // v + 256 i): the rows that see one take note of it, by a product of
 // indicators, so that the codes can lose it before they meet the weights of
@@ -274,14 +378,25 @@ template <int D, int NC> __device__ __forceinline__ void apply_nan(Rows<D, NC>& 
 
 __device__ __forceinline__ uint32_t without_nan(uint32_t x) { return x & ~((nan_bytes(x) >> 7) * 0xffu); }
 
-// dims d..d+3 of row r of the sequence and head; sum is 2^kHead times the numerator
-template <int D>
+// dims d..d+3 of row r of the sequence and head; sum is 2^kHead times the numerator,
+// top its bound
+template <int CODES, int D>
 __device__ __forceinline__ void store_row(const AttendArgs& a, const Span& sp, uint32_t head, uint32_t G, bool bf16,
-                                          uint32_t r, int d, float4v sum, float below) {
+                                          uint32_t r, int d, float4v sum, float below, float top) {
   const uint32_t token = r / G, qh = head * G + r % G;
   const float4v o = below == 0.0f ? float4v{0, 0, 0, 0} : sum * (power_of_two(-kHead) / below);
   const uint2v out = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
   *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = out;
+  // log2 of the sum of 2^x
+  if (a.lse && d == 0)
+    a.lse[(uint64_t)(sp.row0 + token) * a.q_heads + qh] =
+        below == 0.0f ? -INFINITY : (CODES == LTC_E2M1 ? top - 191.0f : top - 64.0f) + __builtin_amdgcn_logf(below * 0x1p64f);
+}
+
+// What a lane has of dims 32 i + 8 g .. + 7 where values are 4-bit codes, in order.
+__device__ __forceinline__ void in_order(float4v a, float4v b, float4v* lo, float4v* hi) {
+  *lo = float4v{a[0], b[0], a[1], b[1]};
+  *hi = float4v{a[2], b[2], a[3], b[3]};
 }
 
 // A denominator of 0 is a row that sees nothing, and keeps its zeros, or one
@@ -332,10 +447,13 @@ constexpr int rows_occupancy(int D, int NC) { return D * NC <= 64 ? 3 : D * NC <
 // at 1,001-6,001 positions (8 heads of 128, 32 query heads) 93 us, 4.6 TB/s, one
 // at 131,071 58 us; by the chain lengths, table, codes, partial results, join
 // where there is not: one at 777 positions 9 us.
-template <bool E4M3, int D, int NC, int W>
+template <int CODES, int D, int NC, int W>
 __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16, uint32_t units, uint32_t splits, uint32_t per_head) {
   constexpr int R = 16 * NC, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
+  constexpr bool kFour = CODES == LTC_E2M1;
+  constexpr uint32_t kBlockBytes = kFour ? 8 * D : 16 * D;  // of 16 tokens' keys or values
+  constexpr int VL = kFour ? DB / 2 : DB;                   // 16 bytes of values: a dim, or two of 4 bits
   __shared__ float lds_acc[W][16][D + 4];
   __shared__ float lds_m[W][R], lds_l[W][R];
   __shared__ bool lds_last;
@@ -366,7 +484,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
 
   const float base = a.scale * kLog2e;
   Rows<D, NC> w;
-  load_rows<D, NC>(w, a, sp, head, G, r0, packed, bf16, n, g);
+  load_rows<CODES, D, NC>(w, a, sp, head, G, r0, packed, bf16, n, g);
   // positions that every row sees need no masks
   const int all_lo = a.window ? max((int)(sp.start + (r1 - 1) / G) + 1 - (int)a.window, 0) : 0;
   const int all_hi = (int)(sp.start + r0 / G) + 1;
@@ -382,13 +500,21 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   auto page_of = [&](int t) -> int32_t { return t < rg.hi ? table[(uint32_t)t >> c.page_log] : -1; };
   auto block_at = [&](int t, int32_t p, bool* have) -> uint64_t {
     *have = (uint32_t)p < c.pages;
-    return head_offset(c, *have ? (uint32_t)p : 0, head) + (((uint32_t)t & page_mask) >> 4) * (16 * D);
+    return head_offset(c, *have ? (uint32_t)p : 0, head) / (kFour ? 2 : 1) + (((uint32_t)t & page_mask) >> 4) * kBlockBytes;
   };
-  uint4v kr[4][KL], vr[DB];
+  uint4v kr[4][KL], vr[VL];
   uint2v kt[4];
-  uint32_t scales;
+  Keys4<D> kq[4];
+  uint32_t scales = 0;
+  uint4v exps[2] = {};  // the bytes of 16 tokens' exponents, keys and values
   bool have_v, next_have_v = false;
-  auto load_k = [&](uint64_t off) {
+  auto load_k = [&](uint64_t off, int t, int32_t page, bool have) {
+    if constexpr (kFour) {
+      const uint8_t* drops = c.scales + token_scales(c, have ? (uint32_t)page : 0, head) + 2 * (page_mask + 1) +
+                             (((uint32_t)t & page_mask) + (n & 3)) * drop_bytes(D);
+      for (int b = 0; b < 4; ++b) kq[b].load(c.k + off + (4 * b + (n & 3)) * 16, drops + 4 * b * drop_bytes(D), g);
+      return;
+    }
     const uint8_t* p = c.k + off + g * 256 + (n & 3) * 16;
     for (int b = 0; b < 4; ++b)
       for (int j = 0; j < KL; ++j) kr[b][j] = *reinterpret_cast<const uint4v*>(p + j * 1024 + b * 64);
@@ -399,10 +525,16 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   };
   auto load_v = [&](uint64_t off) {
     const uint8_t* p = c.v + off + n * 16;
-    for (int i = 0; i < DB; ++i) vr[i] = *reinterpret_cast<const uint4v*>(p + i * 256);
+    for (int i = 0; i < VL; ++i) vr[i] = *reinterpret_cast<const uint4v*>(p + i * 256);
   };
-  auto load_scales = [&](int32_t p, bool have) -> uint32_t {
-    return *reinterpret_cast<const uint16_t*>(c.scales + ((uint64_t)(have ? (uint32_t)p : 0) * c.heads + head) * 2);
+  auto load_scales = [&](int32_t p, int t, bool have) {
+    if constexpr (kFour) {
+      const uint8_t* at = c.scales + token_scales(c, have ? (uint32_t)p : 0, head) + ((uint32_t)t & page_mask);
+      exps[0] = *reinterpret_cast<const uint4v*>(at);
+      exps[1] = *reinterpret_cast<const uint4v*>(at + page_mask + 1);
+    } else {
+      scales = *reinterpret_cast<const uint16_t*>(c.scales + ((uint64_t)(have ? (uint32_t)p : 0) * c.heads + head) * 2);
+    }
   };
 
   // table entries are read a step before the addresses that need them
@@ -414,9 +546,9 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     v_page = page_of(step * kStep + g * 16);
     const uint64_t k_off = block_at(step * kStep + kb * 16, k_page, &have_k);
     v_off = block_at(step * kStep + g * 16, v_page, &next_have_v);
-    load_k(k_off);
+    load_k(k_off, step * kStep + kb * 16, k_page, have_k);
     load_v(v_off);
-    scales = load_scales(v_page, next_have_v);
+    load_scales(v_page, step * kStep + g * 16, next_have_v);
     k_page = page_of((step + W) * kStep + kb * 16);
     v_page = page_of((step + W) * kStep + g * 16);
   }
@@ -424,6 +556,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     const int t0 = step * kStep, tv = t0 + g * 16;
     have_v = next_have_v;
     const uint32_t sc = scales;
+    const uint4v ke = exps[0], ve = exps[1];
     // ---- S^T
     float4v st[NC][4];
     for (int nc = 0; nc < NC; ++nc)
@@ -432,8 +565,10 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
-        const half8 k8 = x < 2 * KL ? codes_to_half<E4M3>(kr[b][x / 2][(x & 1) * 2], kr[b][x / 2][(x & 1) * 2 + 1])
-                                    : codes_to_half<E4M3>(kt[b][0], kt[b][1]);
+        half8 k8;
+        if constexpr (kFour) k8 = kq[b].half(x, g);
+        else if (x < 2 * KL) k8 = codes_to_half<CODES>(kr[b][x / 2][(x & 1) * 2], kr[b][x / 2][(x & 1) * 2 + 1]);
+        else k8 = codes_to_half<CODES>(kt[b][0], kt[b][1]);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
           st[nc][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w.q[nc][x], st[nc][b], 0, 0, 0);
@@ -443,8 +578,8 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     if (next < step_end) {
       const uint64_t k_off = block_at(next * kStep + kb * 16, k_page, &have_k);
       next_v = block_at(next * kStep + g * 16, v_page, &next_have_v);
-      load_k(k_off);
-      scales = load_scales(v_page, next_have_v);
+      load_k(k_off, next * kStep + kb * 16, k_page, have_k);
+      load_scales(v_page, next * kStep + g * 16, next_have_v);
       k_page = page_of((next + W) * kStep + kb * 16);
       v_page = page_of((next + W) * kStep + g * 16);
     }
@@ -453,15 +588,16 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     if (lost && n == 0) report(c, kCacheBadPage);
     const bool edge = t0 < all_lo || t0 + kStep > all_hi || __any(lost);
     half8 p[NC][2];
-    step_weights<D, NC>(w, st, p, base, sc, tv, edge, have_v);
+    if constexpr (kFour) step_weights4<D, NC>(w, st, p, base, ke, ve, tv, edge, have_v);
+    else step_weights<D, NC>(w, st, p, base, sc, tv, edge, have_v);
     // ---- O^T
-    if (edge) {
+    if (edge && !kFour) {
       // codes that no row sees may be anything, and 0 * NaN is NaN
       for (int dw = 0; dw < 4; ++dw) {
         const uint32_t keep = have_v ? byte_mask(tv + 4 * dw, rg.lo, rg.hi) : 0;
         for (int i = 0; i < DB; ++i) vr[i][dw] &= keep;
       }
-      if constexpr (E4M3) {
+      if constexpr (CODES == LTC_E4M3) {
         uint32_t any = 0;
         for (int i = 0; i < DB; ++i)
           for (int dw = 0; dw < 4; ++dw) any |= nan_bytes(vr[i][dw]);
@@ -479,7 +615,9 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     for (int i = 0; i < DB; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const half8 v8 = codes_to_half<E4M3>(vr[i][2 * h], vr[i][2 * h + 1]);
+        half8 v8;
+        if constexpr (kFour) v8 = codes4_to_half(vr[i / 2][2 * (i & 1) + h], 1.0f);
+        else v8 = codes_to_half<CODES>(vr[i][2 * h], vr[i][2 * h + 1]);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
           w.acc[nc][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p[nc][h], w.acc[nc][i], 0, 0, 0);
@@ -488,7 +626,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     if (next < step_end) load_v(v_off);
   }
 
-  if constexpr (E4M3) apply_nan<D, NC>(w);
+  if constexpr (CODES == LTC_E4M3) apply_nan<D, NC>(w);
   // ---- the waves' parts together
   for (int nc = 0; nc < NC; ++nc) {
     w.l[nc] += __shfl_xor(w.l[nc], 16);
@@ -509,9 +647,18 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
       float top = -INFINITY;
       for (int v = 0; v < W; ++v) top = fmaxf(top, lds_m[v][r]);
       const float keep = w.m[nc] == top ? 1.0f : __builtin_amdgcn_exp2f(w.m[nc] - top);
-      for (int i = 0; i < DB; ++i) {
-        const float4v x = w.acc[nc][i] * keep;
-        *reinterpret_cast<float4v*>(&lds_acc[wave][n][i * 16 + 4 * g]) = x;
+      if constexpr (kFour) {
+        for (int i = 0; i < DB; i += 2) {
+          float4v lo, hi;
+          in_order(w.acc[nc][i] * keep, w.acc[nc][i + 1] * keep, &lo, &hi);
+          *reinterpret_cast<float4v*>(&lds_acc[wave][n][i * 16 + 8 * g]) = lo;
+          *reinterpret_cast<float4v*>(&lds_acc[wave][n][i * 16 + 8 * g + 4]) = hi;
+        }
+      } else {
+        for (int i = 0; i < DB; ++i) {
+          const float4v x = w.acc[nc][i] * keep;
+          *reinterpret_cast<float4v*>(&lds_acc[wave][n][i * 16 + 4 * g]) = x;
+        }
       }
     }
     __syncthreads();
@@ -529,7 +676,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
         put2(part + (at + r) * D + d + 2, sum[2], sum[3]);
         if (d == 0) put2(part_ml + (at + r) * 2, top, below);
       } else {
-        store_row<D>(a, sp, head, G, bf16, r0 + r, d, sum, below);
+        store_row<CODES, D>(a, sp, head, G, bf16, r0 + r, d, sum, below, top);
       }
     }
     __syncthreads();
@@ -616,7 +763,8 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
       float below[RA];
       gather(std::integral_constant<int, RA>(), std::integral_constant<int, 4>(), r, GROUPS, 0, 1, sum, below);
       for (int k = 0; k < RA; ++k)
-        if (r + k * GROUPS < live) store_row<D>(a, sp, head, G, bf16, r0 + r + k * GROUPS, x * 4, sum[k], below[k]);
+        if (r + k * GROUPS < live)
+          store_row<CODES, D>(a, sp, head, G, bf16, r0 + r + k * GROUPS, x * 4, sum[k], below[k], lds_m[0][r + k * GROUPS]);
     }
     spoil();
     return;
@@ -637,7 +785,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
       sum += *reinterpret_cast<const float4v*>(lds_flat + ((grp + i) * LANES + x) * 4);
       below += lds_l[0][grp + i];
     }
-    store_row<D>(a, sp, head, G, bf16, r0 + row, x * 4, sum, below);
+    store_row<CODES, D>(a, sp, head, G, bf16, r0 + row, x * 4, sum, below, lds_m[0][row]);
   }
   spoil();
 }
@@ -672,11 +820,14 @@ template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
 // turning 12% faster, without loads 14%, with an eighth of the second product
 // 10%: the chain of a step (read, product, maximum, exp2, product) is longer
 // than two waves a SIMD hide.
-template <bool E4M3, int D>
+template <int CODES, int D>
 __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
                                                                           AttendArgs a, bool bf16, uint32_t units,
                                                                           uint32_t per_head) {
-  constexpr int NC = 2, WR = 16 * NC, R = kTileRows, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16, VL = (DB + 3) / 4;
+  constexpr int NC = 2, WR = 16 * NC, R = kTileRows, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
+  constexpr bool kFour = CODES == LTC_E2M1;
+  constexpr uint32_t kBlockBytes = kFour ? 8 * D : 16 * D;
+  constexpr int VB = kFour ? DB / 2 : DB, VL = (VB + 3) / 4;
   __shared__ half8 lds[2][(KS * 4 + DB * 2) * 64];  // keys [x][b][lane], values [i][h][lane]
   __shared__ int lds_nan[2];                        // 1 + the step whose values have a NaN
   constexpr int kValues = KS * 4;
@@ -709,18 +860,22 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
   const int hi = live ? (int)(sp.start + (w1 - 1) / G) + 1 : 0, all_hi = live ? (int)(sp.start + w0 / G) + 1 : 0;
   const int lo = a.window ? max(all_hi - (int)a.window, 0) : 0, all_lo = a.window ? max(hi - (int)a.window, 0) : 0;
   Rows<D, NC> w;
-  load_rows<D, NC>(w, a, sp, head, G, w0, packed, bf16, n, g);
+  load_rows<CODES, D, NC>(w, a, sp, head, G, w0, packed, bf16, n, g);
 
   const uint32_t page_mask = (1u << c.page_log) - 1;
   const int kb = n >> 2;
   const int32_t* table = s.table + seq * s.table_stride;
   auto page_of = [&](int t) -> int32_t { return t < rg.hi ? table[(uint32_t)t >> c.page_log] : -1; };
   auto block_at = [&](int t, int32_t p) -> uint64_t {
-    return head_offset(c, (uint32_t)p < c.pages ? (uint32_t)p : 0, head) + (((uint32_t)t & page_mask) >> 4) * (16 * D);
+    return head_offset(c, (uint32_t)p < c.pages ? (uint32_t)p : 0, head) / (kFour ? 2 : 1) +
+           (((uint32_t)t & page_mask) >> 4) * kBlockBytes;
   };
-  // a quarter of a step's codes: block b = wave of the keys, dims 16 i + n of the values, i = wave, wave + 4 ..
+  // a quarter of a step's codes: block b = wave of the keys, dims 16 i + n of the values (of 4 bits 32 i + 2 n and
+  // one on), i = wave, wave + 4 ..
   uint4v kr[KL], vr[VL];
   uint2v kt = {0, 0};
+  Keys4<D> kq;
+  uint4v exps[2] = {}, next_exps[2] = {};  // of the step computed, and of the next one, at g's tokens
   int32_t k_page = -1, v_page = -1;           // of the step to load next
   int32_t page = -1, next_page = -1;          // of the step computed, and of the next one, at g's tokens
   uint32_t scales = 0, next_scales = 0;
@@ -731,21 +886,38 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
   auto load = [&](int step) {
     const uint8_t* k = c.k + block_at(step * kStep + kb * 16, k_page) + (n & 3) * 16 + wave * 64;
     const uint8_t* v = c.v + block_at(step * kStep + g * 16, v_page) + n * 16;
-    for (int j = 0; j < KL; ++j) kr[j] = *reinterpret_cast<const uint4v*>(k + g * 256 + j * 1024);
-    if constexpr (TAIL) kt = *reinterpret_cast<const uint2v*>(k + KL * 1024 + (g >> 1) * 256 + (g & 1) * 8);
+    if constexpr (kFour) {
+      const int tk = step * kStep + kb * 16, tv = step * kStep + g * 16;
+      const uint8_t* sk = c.scales + token_scales(c, (uint32_t)k_page < c.pages ? (uint32_t)k_page : 0, head);
+      const uint8_t* sv = c.scales + token_scales(c, (uint32_t)v_page < c.pages ? (uint32_t)v_page : 0, head);
+      kq.load(k, sk + 2 * (page_mask + 1) + (((uint32_t)tk & page_mask) + (n & 3) + 4 * wave) * drop_bytes(D), g);
+      next_exps[0] = *reinterpret_cast<const uint4v*>(sv + ((uint32_t)tv & page_mask));
+      next_exps[1] = *reinterpret_cast<const uint4v*>(sv + ((uint32_t)tv & page_mask) + page_mask + 1);
+    } else {
+      for (int j = 0; j < KL; ++j) kr[j] = *reinterpret_cast<const uint4v*>(k + g * 256 + j * 1024);
+      if constexpr (TAIL) kt = *reinterpret_cast<const uint2v*>(k + KL * 1024 + (g >> 1) * 256 + (g & 1) * 8);
+    }
     for (int i = 0; i < VL; ++i)
-      if (DB % 4 == 0 || wave + 4 * i < DB) vr[i] = *reinterpret_cast<const uint4v*>(v + (wave + 4 * i) * 256);
+      if (VB % 4 == 0 || wave + 4 * i < VB) vr[i] = *reinterpret_cast<const uint4v*>(v + (wave + 4 * i) * 256);
     next_page = v_page;
-    next_scales = *reinterpret_cast<const uint16_t*>(
-        c.scales + ((uint64_t)((uint32_t)v_page < c.pages ? (uint32_t)v_page : 0) * c.heads + head) * 2);
+    if constexpr (!kFour)
+      next_scales = *reinterpret_cast<const uint16_t*>(
+          c.scales + ((uint64_t)((uint32_t)v_page < c.pages ? (uint32_t)v_page : 0) * c.heads + head) * 2);
     pages(step + 1);
   };
   auto turn = [&](int step) {
     half8* to = lds[step & 1] + lane;
+    if constexpr (kFour) {
+      for (int x = 0; x < KS; ++x) to[(x * 4 + wave) * 64] = kq.half(x, g);
+      for (int i = 0; i < VL; ++i)
+        if (VB % 4 == 0 || wave + 4 * i < VB)
+          for (int h = 0; h < 4; ++h) to[(kValues + 4 * (wave + 4 * i) + h) * 64] = codes4_to_half(vr[i][h], 1.0f);
+      return;
+    }
     for (int j = 0; j < KL; ++j)
       for (int x = 0; x < 2; ++x)
-        to[((2 * j + x) * 4 + wave) * 64] = codes_to_half<E4M3>(kr[j][2 * x], kr[j][2 * x + 1]);
-    if constexpr (TAIL) to[((KS - 1) * 4 + wave) * 64] = codes_to_half<E4M3>(kt[0], kt[1]);
+        to[((2 * j + x) * 4 + wave) * 64] = codes_to_half<CODES>(kr[j][2 * x], kr[j][2 * x + 1]);
+    if constexpr (TAIL) to[((KS - 1) * 4 + wave) * 64] = codes_to_half<CODES>(kt[0], kt[1]);
     // values that no row sees may be anything, and 0 * NaN is NaN
     const int t0 = step * kStep, tv = t0 + g * 16;
     const bool lost = (uint32_t)next_page >= c.pages;
@@ -754,7 +926,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
         const uint32_t keep = lost ? 0 : byte_mask(tv + 4 * dw, rg.lo, rg.hi);
         for (int i = 0; i < VL; ++i) vr[i][dw] &= keep;
       }
-    if constexpr (E4M3) {
+    if constexpr (CODES == LTC_E4M3) {
       uint32_t any = 0;
       for (int i = 0; i < VL; ++i)
         for (int dw = 0; dw < 4; ++dw) any |= nan_bytes(vr[i][dw]);
@@ -767,7 +939,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
     for (int i = 0; i < VL; ++i)
       if (DB % 4 == 0 || wave + 4 * i < DB)
         for (int h = 0; h < 2; ++h)
-          to[(kValues + 2 * (wave + 4 * i) + h) * 64] = codes_to_half<E4M3>(vr[i][2 * h], vr[i][2 * h + 1]);
+          to[(kValues + 2 * (wave + 4 * i) + h) * 64] = codes_to_half<CODES>(vr[i][2 * h], vr[i][2 * h + 1]);
   };
 
   int step = rg.first;
@@ -781,6 +953,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
     turn(step);
     page = next_page;
     scales = next_scales;
+    for (int i = 0; i < 2; ++i) exps[i] = next_exps[i];
     if (step + 1 < step_end) load(step + 1);
   }
   for (; step < step_end; ++step) {
@@ -788,10 +961,12 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
     const int32_t p_now = page;
     const bool have = (uint32_t)p_now < c.pages;
     const uint32_t sc = scales;
+    const uint4v ke = exps[0], ve = exps[1];
     if (step + 1 < step_end) {
       turn(step + 1);
       page = next_page;
       scales = next_scales;
+      for (int i = 0; i < 2; ++i) exps[i] = next_exps[i];
       if (step + 2 < step_end) load(step + 2);
     }
     const int t0 = step * kStep, tv = t0 + g * 16;
@@ -816,7 +991,8 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
     if (lost && n == 0) report(c, kCacheBadPage);
     const bool edge = t0 < all_lo || t0 + kStep > all_hi || __any(lost);
     half8 p[NC][2];
-    step_weights<D, NC>(w, st, p, base, sc, tv, edge, have);
+    if constexpr (kFour) step_weights4<D, NC>(w, st, p, base, ke, ve, tv, edge, have);
+    else step_weights<D, NC>(w, st, p, base, sc, tv, edge, have);
     // ---- O^T
     from += kValues * 64;
 #pragma unroll
@@ -831,16 +1007,26 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
             w.acc[nc][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p[nc][h], w.acc[nc][j], 0, 0, 0);
         }
     reads_ahead<DB / 2, NC>();
-    if (E4M3 && lds_nan[step & 1] == step + 1) note_nan<D, NC>(w, tv, have, c.v + block_at(tv, p_now) + n * 16);
+    if (CODES == LTC_E4M3 && lds_nan[step & 1] == step + 1) note_nan<D, NC>(w, tv, have, c.v + block_at(tv, p_now) + n * 16);
   }
-  if constexpr (E4M3) apply_nan<D, NC>(w);
+  if constexpr (CODES == LTC_E4M3) apply_nan<D, NC>(w);
   for (int nc = 0; nc < NC; ++nc) {
     float below = w.l[nc];
     below += __shfl_xor(below, 16);
     below += __shfl_xor(below, 32);
     const uint32_t r = w0 + nc * 16 + n;
-    if (r < packed)
-      for (int i = 0; i < DB; ++i) store_row<D>(a, sp, head, G, bf16, r, i * 16 + 4 * g, w.acc[nc][i], below);
+    if (r < packed) {
+      if constexpr (kFour) {
+        for (int i = 0; i < DB; i += 2) {
+          float4v lo, hi;
+          in_order(w.acc[nc][i], w.acc[nc][i + 1], &lo, &hi);
+          store_row<CODES, D>(a, sp, head, G, bf16, r, i * 16 + 8 * g, lo, below, w.m[nc]);
+          store_row<CODES, D>(a, sp, head, G, bf16, r, i * 16 + 8 * g + 4, hi, below, w.m[nc]);
+        }
+      } else {
+        for (int i = 0; i < DB; ++i) store_row<CODES, D>(a, sp, head, G, bf16, r, i * 16 + 4 * g, w.acc[nc][i], below, w.m[nc]);
+      }
+    }
     spoil_rows<D>(c, a, sp, table, head, G, r, g == 0 && r < packed && below == 0.0f);
   }
 }
@@ -895,22 +1081,22 @@ Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t 
   return p;
 }
 
-template <bool E4M3, int D, int W>
+template <int CODES, int D, int W>
 hipError_t launch_waves(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
                         hipStream_t st) {
   auto launch = [&](auto kernel) {
     kernel<<<p.grid, 64 * W, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
   };
-  if (p.nc == 1) launch(k_attend_rows<E4M3, D, 1, W>);
-  else if constexpr (D <= 192) launch(k_attend_rows<E4M3, D, 2, W>);
+  if (p.nc == 1) launch(k_attend_rows<CODES, D, 1, W>);
+  else if constexpr (D <= 192) launch(k_attend_rows<CODES, D, 2, W>);
   return hipGetLastError();
 }
 
-template <bool E4M3, int D>
+template <int CODES, int D>
 hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
                        hipStream_t st) {
   if (p.tiles) {
-    k_attend_tiles<E4M3, D><<<p.grid, 256, 0, st>>>(c, s, p.map, a, bf16, p.units, p.per_head);
+    k_attend_tiles<CODES, D><<<p.grid, 256, 0, st>>>(c, s, p.map, a, bf16, p.units, p.per_head);
     return hipGetLastError();
   }
   // Heads of 192 and 256 dims leave a SIMD one wave: where nothing is split, two
@@ -919,36 +1105,24 @@ hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const At
   // 143 / 176 us, 64 at 1,000-6,000 194 / 192 us.  With 128 dims: 62 / 72 us and
   // 113 / 92 us, so four there.
   if constexpr (D >= 192) {
-    if (p.splits == 1) return launch_waves<E4M3, D, 2>(c, s, bf16, a, p, st);
+    if (p.splits == 1) return launch_waves<CODES, D, 2>(c, s, bf16, a, p, st);
   }
-  return launch_waves<E4M3, D, kWaves>(c, s, bf16, a, p, st);
-}
-
-template <bool E4M3>
-hipError_t launch_dim(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, hipStream_t st) {
-  const Plan p = plan_rows(c, s, a.q_heads, a.window);
-  switch (c.dim) {
-    case 64: return launch_rows<E4M3, 64>(c, s, bf16, a, p, st);
-    case 96: return launch_rows<E4M3, 96>(c, s, bf16, a, p, st);
-    case 128: return launch_rows<E4M3, 128>(c, s, bf16, a, p, st);
-    case 192: return launch_rows<E4M3, 192>(c, s, bf16, a, p, st);
-    case 256: return launch_rows<E4M3, 256>(c, s, bf16, a, p, st);
-  }
-  return hipErrorInvalidValue;
+  return launch_waves<CODES, D, kWaves>(c, s, bf16, a, p, st);
 }
 
 }  // namespace
 
-uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
-  if (!s.rows) return 0;
-  const Plan p = plan_rows(c, s, q_heads, window);
-  return p.splits == 1 ? 0 : kCounterBytes + (uint64_t)p.units * c.heads * p.splits * 16 * p.nc * (c.dim + 2) * sizeof(float);
-}
-
-hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, bool e4m3, int dtype, const AttendArgs& a,
-                               hipStream_t st) {
-  const bool bf16 = dtype == LTC_BF16;
-  return e4m3 ? launch_dim<true>(c, s, bf16, a, st) : launch_dim<false>(c, s, bf16, a, st);
+template <int CODES>
+hipError_t launch_attend(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, hipStream_t st) {
+  const Plan p = plan_rows(c, s, a.q_heads, a.window);
+  switch (c.dim) {
+    case 64: return launch_rows<CODES, 64>(c, s, bf16, a, p, st);
+    case 96: return launch_rows<CODES, 96>(c, s, bf16, a, p, st);
+    case 128: return launch_rows<CODES, 128>(c, s, bf16, a, p, st);
+    case 192: return launch_rows<CODES, 192>(c, s, bf16, a, p, st);
+    case 256: return launch_rows<CODES, 256>(c, s, bf16, a, p, st);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace ltc

@@ -1,6 +1,8 @@
 // ltc_cache_device.h -- device helpers shared by the cache's kernels.
 #pragma once
 
+#include <type_traits>
+
 #include "ltc_cache_launch.h"
 #include "ltc_internal.h"
 
@@ -102,6 +104,63 @@ __device__ __forceinline__ void clear_unnamed(const Unnamed& u, uint16_t* out, u
     *reinterpret_cast<uint4v*>(out + unnamed_row(u, (uint32_t)(i / parts)) * stride + i % parts * 8) = uint4v{0, 0, 0, 0};
 }
 
+// A wave's share of keys: token lane & 15, dims of part 4 j + lane / 16.
+// A wave's share of values: tokens 4 (lane / 16) + i, dims 64 j + 4 (lane & 15) + 0..3.
+template <int D> struct Share {
+  static constexpr int J = (D + 63) / 64;
+  // of the last 64 dims, D = 96 has only the first 32
+  static __device__ __forceinline__ bool k_has(int j, int lane) { return D % 64 == 0 || j < J - 1 || lane < 32; }
+  static __device__ __forceinline__ bool v_has(int j, int lane) { return D % 64 == 0 || j < J - 1 || (lane & 15) < 8; }
+};
+
+typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+
+// largest magnitudes (as bits) of the pairs' halves
+__device__ __forceinline__ ushort2v max_bits(ushort2v top, uint32_t pair) {
+  return __builtin_elementwise_max(top, __builtin_bit_cast(ushort2v, pair & 0x7fff7fffu));
+}
+
+// the same without infinities and NaN
+template <uint32_t kInf> __device__ __forceinline__ uint32_t max_finite_bits(uint32_t top, uint32_t pair) {
+  uint32_t mask = 0x7fffu;
+  asm("" : "+v"(mask));  // no common subexpressions with max_bits: they would be kept in registers for this rare case
+  const uint32_t lo = pair & mask, hi = pair >> 16 & mask;
+  return max(top, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
+}
+
+template <int DT> __device__ __forceinline__ float4v widen4(uint2v x) {
+  return float4v{widen<DT>(x[0] & 0xffffu), widen<DT>(x[0] >> 16), widen<DT>(x[1] & 0xffffu), widen<DT>(x[1] >> 16)};
+}
+
+template <int BYTES> __device__ __forceinline__ uint32_t load_drops(const uint8_t* at) {
+  if constexpr (BYTES == 4) return *reinterpret_cast<const uint32_t*>(at);
+  else if constexpr (BYTES == 2) return *reinterpret_cast<const uint16_t*>(at);
+  else return *at;
+}
+
 __device__ __forceinline__ void report(const CacheView& c, uint32_t bit) { atomicOr(c.status, bit); }
+
+// ---- on the host
+
+inline UnitMap page_units(const CacheView& c, const SeqView& s) {
+  if (!s.cu) return UnitMap{0, 1, 1};  // one row, one page
+  return UnitMap{1, 1u << c.page_log, 2};
+}
+
+// f with the numbers' and the head's types as constants
+template <class F> hipError_t for_numbers(int dtype, uint32_t dim, F f) {
+  auto with_dim = [&](auto type) {
+    switch (dim) {
+      case 64: return f(type, std::integral_constant<int, 64>()), hipGetLastError();
+      case 96: return f(type, std::integral_constant<int, 96>()), hipGetLastError();
+      case 128: return f(type, std::integral_constant<int, 128>()), hipGetLastError();
+      case 192: return f(type, std::integral_constant<int, 192>()), hipGetLastError();
+      case 256: return f(type, std::integral_constant<int, 256>()), hipGetLastError();
+    }
+    return hipErrorInvalidValue;
+  };
+  return dtype == LTC_BF16 ? with_dim(std::integral_constant<int, LTC_BF16>())
+                           : with_dim(std::integral_constant<int, LTC_FP16>());
+}
 
 }  // namespace ltc

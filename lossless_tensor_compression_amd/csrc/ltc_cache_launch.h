@@ -14,11 +14,17 @@ struct RowsView {
   uint64_t row_stride, head_stride;
 };
 
+// codes of 8 bits, and of 4
 hipError_t launch_cache_write(const CacheView& c, const SeqView& s, bool e4m3, int dtype, const RowsView& k,
                               const RowsView& v, hipStream_t st);
 
 hipError_t launch_cache_read(const CacheView& c, const SeqView& s, bool e4m3, int dtype, uint16_t* k, uint16_t* v,
                              hipStream_t st);
+
+hipError_t launch_cache4_write(const CacheView& c, const SeqView& s, int dtype, const RowsView& k, const RowsView& v,
+                               hipStream_t st);
+
+hipError_t launch_cache4_read(const CacheView& c, const SeqView& s, int dtype, uint16_t* k, uint16_t* v, hipStream_t st);
 
 struct AttendArgs {
   RowsView q;
@@ -27,11 +33,16 @@ struct AttendArgs {
   uint32_t window;  // 0: all positions up to the row's own
   float scale;      // of the products before the softmax
   void* ws;
+  float* lse;  // [rows][q_heads] log2 of the softmax's sum, or null
 };
 
 uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window);
 
-hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, bool e4m3, int dtype, const AttendArgs& a,
+hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, int codes, int dtype, const AttendArgs& a,
                                hipStream_t st);
+
+// of one code type; each is built in a file of its own
+template <int CODES>
+hipError_t launch_attend(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, hipStream_t st);
 
 }  // namespace ltc

@@ -13,34 +13,6 @@ namespace {
 // 8 heads of 128.  So 28 us, 4.4 TB/s, and 84 us, 4.8
 // TB/s, where a 2 GiB copy runs at 4.9; a token of each of 48 sequences 6 us.
 
-// A wave's share of keys: token lane & 15, dims of part 4 j + lane / 16.
-// A wave's share of values: tokens 4 (lane / 16) + i, dims 64 j + 4 (lane & 15) + 0..3.
-template <int D> struct Share {
-  static constexpr int J = (D + 63) / 64;
-  // of the last 64 dims, D = 96 has only the first 32
-  static __device__ __forceinline__ bool k_has(int j, int lane) { return D % 64 == 0 || j < J - 1 || lane < 32; }
-  static __device__ __forceinline__ bool v_has(int j, int lane) { return D % 64 == 0 || j < J - 1 || (lane & 15) < 8; }
-};
-
-typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
-
-// largest magnitudes (as bits) of the pairs' halves
-__device__ __forceinline__ ushort2v max_bits(ushort2v top, uint32_t pair) {
-  return __builtin_elementwise_max(top, __builtin_bit_cast(ushort2v, pair & 0x7fff7fffu));
-}
-
-// the same without infinities and NaN
-template <uint32_t kInf> __device__ __forceinline__ uint32_t max_finite_bits(uint32_t top, uint32_t pair) {
-  uint32_t mask = 0x7fffu;
-  asm("" : "+v"(mask));  // no common subexpressions with max_bits: they would be kept in registers for this rare case
-  const uint32_t lo = pair & mask, hi = pair >> 16 & mask;
-  return max(top, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
-}
-
-template <int DT> __device__ __forceinline__ float4v widen4(uint2v x) {
-  return float4v{widen<DT>(x[0] & 0xffffu), widen<DT>(x[0] >> 16), widen<DT>(x[1] & 0xffffu), widen<DT>(x[1] >> 16)};
-}
-
 // The page's new rows set the scale; a page that already holds tokens of the
 // sequence keeps the larger of its scale and theirs, and if that grew, its
 // tokens are coded again.
@@ -265,11 +237,6 @@ __global__ __launch_bounds__(1024) void k_cache_read(CacheView c, SeqView s, Uni
   }
 }
 
-UnitMap page_units(const CacheView& c, const SeqView& s) {
-  if (!s.cu) return UnitMap{0, 1, 1};  // one row, one page
-  return UnitMap{1, 1u << c.page_log, 2};
-}
-
 template <bool E4M3, int DT, int D>
 void launch_write(const CacheView& c, const SeqView& s, const RowsView& k, const RowsView& v, hipStream_t st) {
   const UnitMap m = page_units(c, s);
@@ -286,21 +253,8 @@ void launch_read(const CacheView& c, const SeqView& s, uint16_t* k, uint16_t* v,
 
 // f with the codes', the numbers' and the head's types as constants
 template <class F> hipError_t for_types(bool e4m3, int dtype, uint32_t dim, F f) {
-  auto with_dim = [&](auto codes, auto type) {
-    switch (dim) {
-      case 64: return f(codes, type, std::integral_constant<int, 64>()), hipGetLastError();
-      case 96: return f(codes, type, std::integral_constant<int, 96>()), hipGetLastError();
-      case 128: return f(codes, type, std::integral_constant<int, 128>()), hipGetLastError();
-      case 192: return f(codes, type, std::integral_constant<int, 192>()), hipGetLastError();
-      case 256: return f(codes, type, std::integral_constant<int, 256>()), hipGetLastError();
-    }
-    return hipErrorInvalidValue;
-  };
-  auto with_type = [&](auto codes) {
-    return dtype == LTC_BF16 ? with_dim(codes, std::integral_constant<int, LTC_BF16>())
-                             : with_dim(codes, std::integral_constant<int, LTC_FP16>());
-  };
-  return e4m3 ? with_type(std::true_type()) : with_type(std::false_type());
+  return e4m3 ? for_numbers(dtype, dim, [&](auto type, auto d) { f(std::true_type(), type, d); })
+              : for_numbers(dtype, dim, [&](auto type, auto d) { f(std::false_type(), type, d); });
 }
 
 }  // namespace

@@ -28,11 +28,12 @@ import torch
 
 from . import LTCError, _check, lib
 
-E4M3, INT8 = 0, 1
-CODES = {"e4m3": E4M3, "int8": INT8}
+E4M3, INT8, E2M1 = 0, 1, 3
+CODES = {"e4m3": E4M3, "int8": INT8, "e2m1": E2M1}
 CACHE_DTYPES = {torch.bfloat16: 1, torch.float16: 2}
 PAGES = (16, 32, 64, 128, 256)
 DIMS = (64, 96, 128, 192, 256)
+DROP_BYTES = {64: 1, 96: 2, 128: 2, 192: 4, 256: 4}  # a token's, of E2M1 codes
 BAD_PAGE, BAD_SEQUENCE = 1, 2
 WS_ZEROS = 65536
 
@@ -57,7 +58,12 @@ class KVCache:
     v_codes uint8 [pages, heads, page/16, dim, 16 tokens]
     scales  uint8 [pages, heads, 2], a scale is 2^(byte - 127)
     dtype: torch.bfloat16 or torch.float16, of keys, values, queries and
-    outputs; codes: "e4m3" or "int8"."""
+    outputs; codes: "e4m3", "int8" or, in 4 bits, "e2m1":
+    k_codes uint8 [pages, heads, page/16, dim/32, 16 tokens, 16], two dims a byte
+    v_codes uint8 [pages, heads, page/16, dim, 8], two tokens a byte
+    scales  uint8 [pages, heads, page * (2 + DROP_BYTES[dim])]: exponents of
+            the tokens' keys, of their values, and for each token a nibble for
+            each 32 dims of its key, how far below its scale theirs is"""
 
     def __init__(self, k_codes, v_codes, scales, dtype, codes):
         if codes not in CODES:
@@ -69,7 +75,7 @@ class KVCache:
                 raise ValueError(f"{name} must be on the cache's GPU")
             if t.dtype != torch.uint8 or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous uint8")
-        pages, heads, page, dim = self._shape(k_codes, v_codes, scales)
+        pages, heads, page, dim = self._shape(k_codes, v_codes, scales, codes)
         self.k_codes, self.v_codes, self.scales = k_codes, v_codes, scales
         self.pages, self.heads, self.page, self.dim = pages, heads, page, dim
         self.dtype, self.codes, self.device = dtype, codes, k_codes.device
@@ -83,21 +89,24 @@ class KVCache:
         self._lock = threading.Lock()  # from a workspace's lookup to the launch that uses it
 
     @staticmethod
-    def _shape(k_codes, v_codes, scales):
+    def _shape(k_codes, v_codes, scales, codes):
+        four = codes == "e2m1"
+        part, tokens = (32, 8) if four else (16, 16)  # dims of 16 bytes of keys, bytes of 16 tokens of values
         if k_codes.dim() != 6 or k_codes.shape[4:] != (16, 16):
-            raise ValueError("k_codes must be [pages, heads, page/16, dim/16, 16, 16]")
+            raise ValueError(f"k_codes must be [pages, heads, page/16, dim/{part}, 16, 16]")
         pages, heads, blocks, parts = k_codes.shape[:4]
-        if v_codes.shape != (pages, heads, blocks, parts * 16, 16):
-            raise ValueError("v_codes must be [pages, heads, page/16, dim, 16]")
-        if scales.shape != (pages, heads, 2):
-            raise ValueError("scales must be [pages, heads, 2]")
+        if v_codes.shape != (pages, heads, blocks, parts * part, tokens):
+            raise ValueError(f"v_codes must be [pages, heads, page/16, dim, {tokens}]")
         if blocks * 16 not in PAGES:
             raise ValueError(f"a page must have one of {PAGES} tokens")
-        if parts * 16 not in DIMS:
+        if parts * part not in DIMS:
             raise ValueError(f"a head must have one of {DIMS} dims")
+        wide = blocks * 16 * (2 + DROP_BYTES[parts * part]) if four else 2
+        if scales.shape != (pages, heads, wide):
+            raise ValueError(f"scales must be [pages, heads, {wide}]")
         if heads < 1:
             raise ValueError("at least one head")
-        return pages, heads, blocks * 16, parts * 16
+        return pages, heads, blocks * 16, parts * part
 
     @classmethod
     def of(cls, k_codes, v_codes, scales, dtype=torch.bfloat16, codes="e4m3"):
@@ -109,8 +118,14 @@ class KVCache:
         """A cache with tensors of its own, zeros with the lowest scale."""
         if page not in PAGES or dim not in DIMS:
             raise ValueError(f"page must be one of {PAGES} and dim one of {DIMS}")
-        return cls(torch.zeros((pages, heads, page // 16, dim // 16, 16, 16), dtype=torch.uint8, device=device),
-                   torch.zeros((pages, heads, page // 16, dim, 16), dtype=torch.uint8, device=device),
+        def zeros(*shape):
+            return torch.zeros((pages, heads, *shape), dtype=torch.uint8, device=device)
+
+        if codes == "e2m1":
+            scales = zeros(page * (2 + DROP_BYTES[dim]))
+            scales[..., :2 * page] = 27
+            return cls(zeros(page // 16, dim // 32, 16, 16), zeros(page // 16, dim, 8), scales, dtype, codes)
+        return cls(zeros(page // 16, dim // 16, 16, 16), zeros(page // 16, dim, 16),
                    torch.full((pages, heads, 2), 27, dtype=torch.uint8, device=device), dtype, codes)
 
     def check(self):
