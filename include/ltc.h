@@ -553,6 +553,27 @@ uint64_t ltc_cache_attend_workspace_size(const ltc_cache* cache, const ltc_cache
 int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
                      uint32_t window, float scale, void* d_out, void* d_ws, uint64_t ws_nbytes, hipStream_t stream);
 
+uint64_t ltc_cache_attend_weigh_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,
+                                               uint32_t window);
+int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
+                           uint32_t window, float scale, void* d_out, float* d_weights, void* d_ws, uint64_t ws_nbytes,
+                           hipStream_t stream);
+
+int ltc_cache_evict(const ltc_cache* cache, const ltc_cache_seqs* seqs, float* d_weights, const int32_t* d_to,
+                    uint64_t to_stride, uint32_t to_width, uint32_t keep, uint32_t recent, int32_t* d_lengths,
+                    int32_t* d_positions, hipStream_t stream);
+
+typedef struct {
+  const uint64_t* d_turns;
+  uint32_t* d_status;
+  uint32_t dim, rotary, pairs;
+  uint32_t reserved;
+} ltc_rotation;
+
+int ltc_norm_rotate(const ltc_rotation* rotation, const ltc_cache_seqs* seqs, int dtype, const ltc_cache_rows* q,
+                    uint32_t q_heads, const void* d_q_weight, const ltc_cache_rows* k, uint32_t k_heads,
+                    const void* d_k_weight, float eps, void* d_q_out, void* d_k_out, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,8 +18,9 @@ API (names as in cuZipNN 0.1.0, "API", and the C ABI):
   compress_delta(t, base) / decompress_delta(blob, base): XOR deltas against
       a base tensor, zero-run coded where the delta is mostly zero bytes
   blob_info / blob_stats for host-side inspection of a blob's header
-  KVCache, cache_write / cache_read / cache_attend: a paged key/value cache in
-      8 bits (kv_cache.py)
+  KVCache, cache_write / cache_read / cache_attend / cache_evict: a paged
+      key/value cache in 8 or 4 bits (kv_cache.py)
+  Rotation, norm_rotate: queries and keys on their way to it (rotation.py)
 """
 import ctypes
 import os
@@ -117,7 +118,13 @@ def lib():
         L.ltc_cache_attend_workspace_size.argtypes = [vp, vp, u32, u32]
         L.ltc_cache_attend_workspace_size.restype = u64
         L.ltc_cache_attend.argtypes = [vp, vp, vp, u32, u32, ctypes.c_float, vp, vp, u64, vp]
+        L.ltc_cache_attend_weigh_workspace_size.argtypes = [vp, vp, u32, u32]
+        L.ltc_cache_attend_weigh_workspace_size.restype = u64
+        L.ltc_cache_attend_weigh.argtypes = [vp, vp, vp, u32, u32, ctypes.c_float, vp, vp, vp, u64, vp]
+        L.ltc_cache_evict.argtypes = [vp, vp, vp, vp, u64, u32, u32, u32, vp, vp, vp]
+        L.ltc_norm_rotate.argtypes = [vp, vp, i32, vp, u32, vp, vp, u32, vp, ctypes.c_float, vp, vp, vp]
         for name in ("ltc_cache_write", "ltc_cache_read", "ltc_cache_attend",
+                     "ltc_cache_attend_weigh", "ltc_cache_evict", "ltc_norm_rotate",
                      "ltc_compress_workspace_size", "ltc_compress_batch_workspace_size",
                      "ltc_compress", "ltc_compress_noalloc", "ltc_compress_batch",
                      "ltc_compress_batch_prof",
@@ -582,4 +589,5 @@ def blob_stats(blob):
     }
 
 
-from .kv_cache import KVCache, cache_attend, cache_read, cache_write  # noqa: E402,F401
+from .kv_cache import KVCache, cache_attend, cache_evict, cache_read, cache_write  # noqa: E402,F401
+from .rotation import Rotation, norm_rotate  # noqa: E402,F401

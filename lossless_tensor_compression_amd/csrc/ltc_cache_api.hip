@@ -12,6 +12,7 @@ constexpr uint32_t kMaxHeads = 65535;      // a grid's second dimension
 // workgroups of an attention are counted in 32 bits
 constexpr uint32_t kMaxRows = 1u << 24;
 constexpr uint32_t kMaxSeqs = 1u << 20;
+constexpr uint32_t kMaxEvictSeqs = 65535, kMaxEvictPages = 65535;  // a grid's further dimensions
 constexpr uint64_t kMaxAttend = 1ull << 31;  // (rows + sequences) * query heads
 
 bool aligned(const void* p, uintptr_t to) { return p && reinterpret_cast<uintptr_t>(p) % to == 0; }
@@ -72,6 +73,33 @@ int check_heads(const CacheView& c, const SeqView& s, uint32_t q_heads) {
   return ((uint64_t)s.rows + s.seqs) * q_heads > kMaxAttend ? LTC_ERR_INVALID_ARGUMENT : LTC_OK;
 }
 
+int check_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
+                 uint32_t window, float scale, void* d_out, CacheView* c, SeqView* s, AttendArgs* a) {
+  int rc = check_cache(cache, c);
+  if (!rc) rc = check_seqs(seqs, s);
+  if (!rc) rc = check_heads(*c, *s, q_heads);
+  if (rc) return rc;
+  if (window > 0x7fffffffu || !(scale > 0.0f && scale < 1e30f)) return LTC_ERR_INVALID_ARGUMENT;
+  if (!s->rows) return LTC_OK;
+  rc = check_rows(q, &a->q);
+  if (rc) return rc;
+  if (!aligned(d_out, 16)) return LTC_ERR_INVALID_ARGUMENT;
+  a->out = static_cast<uint16_t*>(d_out);
+  a->q_heads = q_heads;
+  a->window = window;
+  a->scale = scale;
+  a->ws = nullptr;
+  a->lse = nullptr;
+  return LTC_OK;
+}
+
+// where the rows' sums lie in the workspace of an attention that weighs: behind
+// what the attention uses, and never in the bytes that calls leave zero
+uint64_t lse_offset(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
+  const uint64_t need = cache_attend_workspace(c, s, q_heads, window);
+  return need < LTC_CACHE_WS_ZEROS ? (uint64_t)LTC_CACHE_WS_ZEROS : (need + 255) / 256 * 256;
+}
+
 int launched(hipError_t e) { return e == hipSuccess ? LTC_OK : LTC_ERR_HIP; }
 
 }  // namespace
@@ -121,25 +149,62 @@ int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const l
   CacheView c;
   SeqView s;
   AttendArgs a;
+  const int rc = check_attend(cache, seqs, q, q_heads, window, scale, d_out, &c, &s, &a);
+  if (rc || !s.rows) return rc;
+  const uint64_t need = cache_attend_workspace(c, s, q_heads, window);
+  if (need && (ws_nbytes < need || !aligned(d_ws, 256))) return LTC_ERR_WORKSPACE;
+  a.ws = d_ws;
+  return launched(launch_cache_attend(c, s, cache->codes, cache->dtype, a, stream));
+}
+
+uint64_t ltc_cache_attend_weigh_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,
+                                               uint32_t window) {
+  CacheView c;
+  SeqView s;
+  if (check_cache(cache, &c) || check_seqs(seqs, &s) || check_heads(c, s, q_heads) || !s.rows) return 0;
+  return lse_offset(c, s, q_heads, window) + (uint64_t)s.rows * q_heads * sizeof(float);
+}
+
+int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
+                           uint32_t window, float scale, void* d_out, float* d_weights, void* d_ws, uint64_t ws_nbytes,
+                           hipStream_t stream) {
+  CacheView c;
+  SeqView s;
+  AttendArgs a;
+  const int rc = check_attend(cache, seqs, q, q_heads, window, scale, d_out, &c, &s, &a);
+  if (rc || !s.rows) return rc;
+  if (c.pages && !aligned(d_weights, 4)) return LTC_ERR_INVALID_ARGUMENT;
+  const uint64_t lse = lse_offset(c, s, q_heads, window);
+  if (ws_nbytes < lse + (uint64_t)s.rows * q_heads * sizeof(float) || !aligned(d_ws, 256)) return LTC_ERR_WORKSPACE;
+  a.ws = d_ws;
+  a.lse = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + lse);
+  hipError_t e = launch_cache_attend(c, s, cache->codes, cache->dtype, a, stream);
+  if (e != hipSuccess) return LTC_ERR_HIP;
+  switch (cache->codes) {
+    case LTC_E4M3: e = launch_weigh<LTC_E4M3>(c, s, cache->dtype, a, d_weights, stream); break;
+    case LTC_INT8: e = launch_weigh<LTC_INT8>(c, s, cache->dtype, a, d_weights, stream); break;
+    default: e = launch_weigh<LTC_E2M1>(c, s, cache->dtype, a, d_weights, stream); break;
+  }
+  return launched(e);
+}
+
+int ltc_cache_evict(const ltc_cache* cache, const ltc_cache_seqs* seqs, float* d_weights, const int32_t* d_to,
+                    uint64_t to_stride, uint32_t to_width, uint32_t keep, uint32_t recent, int32_t* d_lengths,
+                    int32_t* d_positions, hipStream_t stream) {
+  CacheView c;
+  SeqView s;
   int rc = check_cache(cache, &c);
   if (!rc) rc = check_seqs(seqs, &s);
   if (rc) return rc;
-  rc = check_heads(c, s, q_heads);
-  if (rc) return rc;
-  if (window > 0x7fffffffu || !(scale > 0.0f && scale < 1e30f)) return LTC_ERR_INVALID_ARGUMENT;
-  if (!s.rows) return LTC_OK;
-  rc = check_rows(q, &a.q);
-  if (rc) return rc;
-  if (!aligned(d_out, 16)) return LTC_ERR_INVALID_ARGUMENT;
-  const uint64_t need = cache_attend_workspace(c, s, q_heads, window);
-  if (need && (ws_nbytes < need || !aligned(d_ws, 256))) return LTC_ERR_WORKSPACE;
-  a.out = static_cast<uint16_t*>(d_out);
-  a.q_heads = q_heads;
-  a.window = window;
-  a.scale = scale;
-  a.ws = d_ws;
-  a.lse = nullptr;
-  return launched(launch_cache_attend(c, s, cache->codes, cache->dtype, a, stream));
+  if (s.cu || s.seqs > kMaxEvictSeqs) return LTC_ERR_INVALID_ARGUMENT;
+  const uint64_t pages = ((uint64_t)keep + cache->page - 1) / cache->page;
+  if (!keep || recent > keep || pages > kMaxEvictPages || to_width < pages || to_stride < to_width)
+    return LTC_ERR_INVALID_ARGUMENT;
+  if (!s.seqs) return LTC_OK;
+  if ((c.pages && !aligned(d_weights, 4)) || !aligned(d_to, 4) || !aligned(d_lengths, 4) || !aligned(d_positions, 4))
+    return LTC_ERR_INVALID_ARGUMENT;
+  const EvictArgs a = {d_weights, d_to, to_stride, keep, recent, d_lengths, d_positions};
+  return launched(launch_cache_evict(c, s, cache->codes, a, stream));
 }
 
 }  // extern "C"

@@ -113,12 +113,12 @@ template <int D> struct Keys4 {
     if constexpr (D % 64) c[D / 32 - 1] = *reinterpret_cast<const uint32_t*>(at + (D / 32 - 1) * 256 + g * 4);
     drops = load_drops<(int)drop_bytes(D)>(drops_at);
   }
-  __device__ __forceinline__ half8 half(int x, int g) const {
+  __device__ __forceinline__ float scale(int x, int g) const {
     constexpr int F = D / 128 * 4, H = D % 128 / 64 * 2;
     const int block = x < F ? x / 4 * 4 + g : x < F + H ? F + (g >> 1) : D / 32 - 1;
-    const uint32_t drop = drops >> (4 * block) & 15;
-    return codes4_to_half(c[x], __builtin_bit_cast(float, ((uint32_t)(127 + kLift) - drop) << 23));
+    return __builtin_bit_cast(float, ((uint32_t)(127 + kLift) - (drops >> (4 * block) & 15)) << 23);
   }
+  __device__ __forceinline__ half8 half(int x, int g) const { return codes4_to_half(c[x], scale(x, g)); }
 };
 
 // Whether any of four E4M3 codes is a NaN (0x7f or 0xff).
@@ -388,9 +388,12 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Span& sp, u
   const uint2v out = {pack2_as(bf16, o[0], o[1]), pack2_as(bf16, o[2], o[3])};
   *reinterpret_cast<uint2v*>(a.out + ((uint64_t)(sp.row0 + token) * a.q_heads + qh) * D + d) = out;
   // log2 of the sum of 2^x
-  if (a.lse && d == 0)
+  if (a.lse && d == 0) {
+    const bool small = below < 0x1p-100f;  // the logarithm takes no subnormal numbers
+    const float log = small ? __builtin_amdgcn_logf(below * 0x1p64f) - 64.0f : __builtin_amdgcn_logf(below);
     a.lse[(uint64_t)(sp.row0 + token) * a.q_heads + qh] =
-        below == 0.0f ? -INFINITY : (CODES == LTC_E2M1 ? top - 191.0f : top - 64.0f) + __builtin_amdgcn_logf(below * 0x1p64f);
+        below == 0.0f ? -INFINITY : (CODES == LTC_E2M1 ? top - 127.0f : top) + log;
+  }
 }
 
 // What a lane has of dims 32 i + 8 g .. + 7 where values are 4-bit codes, in order.
@@ -1047,7 +1050,7 @@ struct Plan {
   dim3 grid;
 };
 
-Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
+inline Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
   Plan p;
   const uint32_t G = q_heads / c.heads;
   const uint64_t mean = ((uint64_t)s.rows * G + s.seqs - 1) / s.seqs;  // packed rows of a sequence and head

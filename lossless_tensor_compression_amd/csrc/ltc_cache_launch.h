@@ -41,6 +41,21 @@ uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, uint32_t q
 hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, int codes, int dtype, const AttendArgs& a,
                                hipStream_t st);
 
+// adds to weights [pages][heads][page] what the rows give the positions they see;
+// a.lse is known
+template <int CODES>
+hipError_t launch_weigh(const CacheView& c, const SeqView& s, int dtype, const AttendArgs& a, float* weights, hipStream_t st);
+
+struct EvictArgs {
+  float* weights;  // [pages][heads][page]
+  const int32_t* to;
+  uint64_t to_stride;
+  uint32_t keep, recent;
+  int32_t *lengths, *positions;
+};
+
+hipError_t launch_cache_evict(const CacheView& c, const SeqView& s, int codes, const EvictArgs& a, hipStream_t st);
+
 // of one code type; each is built in a file of its own
 template <int CODES>
 hipError_t launch_attend(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, hipStream_t st);

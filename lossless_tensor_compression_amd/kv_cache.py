@@ -1,13 +1,16 @@
-"""A paged key/value cache in 8 bits: quantised as it is written, read back,
-and attended to in place.
+"""A paged key/value cache in 8 or 4 bits: quantised as it is written, read
+back, attended to in place, and cut to the positions that were worth most.
 
   KVCache.empty(...) / KVCache.of(...)  the cache's tensors and their layout
   cache_write(cache, k, v, table, lengths, cu)   new keys and values to their positions
   cache_read(cache, table, lengths, cu, rows)    positions back as 16-bit rows
-  cache_attend(cache, q, table, lengths, cu)     attention of new queries
+  cache_attend(cache, q, table, lengths, cu)     attention of new queries; with
+                                                 weights=, what each position got is added up
+  cache_evict(cache, weights, table, lengths, to, keep, recent)
+                                                 the positions of most weight to other pages
 
-A binding over ltc_cache_write, ltc_cache_read and ltc_cache_attend of
-include/ltc.h, where the layouts, the rounding and what happens with bad
+A binding over ltc_cache_write, ltc_cache_read, ltc_cache_attend,
+ltc_cache_attend_weigh and ltc_cache_evict of include/ltc.h, where the layouts, the rounding and what happens with bad
 tables are written down.  Calls run on the current stream, allocate nothing
 but their outputs and a workspace that the cache keeps for each stream, and
 never synchronise, so they can be captured in a graph.  They have no backward
@@ -49,6 +52,22 @@ class CacheStruct(ctypes.Structure):
                 ("d_status", ctypes.c_void_p), ("pages", ctypes.c_uint32), ("heads", ctypes.c_uint32),
                 ("dim", ctypes.c_uint32), ("page", ctypes.c_uint32), ("codes", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+def _take_rows(t, heads, dim, name):
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which the cache's operators have not: call under torch.no_grad()")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [rows, {'heads' if heads is None else heads}, {dim}]")
+    r, h, d = t.stride()
+    at = t.data_ptr()
+    if d != 1 or r % 8 or h % 8 or at % 16:
+        # a plain clone keeps the strides of dimensions of one, whatever they are
+        t = t.clone(memory_format=torch.contiguous_format)
+        r, h, d = t.stride()
+        at = t.data_ptr()
+    return t, _pack_rows(at, r, h), shape
 
 
 class KVCache:
@@ -128,6 +147,10 @@ class KVCache:
         return cls(zeros(page // 16, dim // 16, 16, 16), zeros(page // 16, dim, 16),
                    torch.full((pages, heads, 2), 27, dtype=torch.uint8, device=device), dtype, codes)
 
+    def no_weights(self):
+        """Zeros to add positions' weights to: float32 [pages, heads, page]."""
+        return torch.zeros((self.pages, self.heads, self.page), dtype=torch.float32, device=self.device)
+
     def check(self):
         """Raises if a call since the last check met a bad page or sequence
         (waits for the GPU)."""
@@ -177,24 +200,21 @@ class KVCache:
         return _pack_seqs(table.data_ptr(), lengths.data_ptr(), 0 if cu is None else cu.data_ptr(), step,
                           seqs, rows, width, 0)
 
+    def _weights(self, t):
+        if t.dtype is not torch.float32 or t.get_device() != self._index or not t.is_contiguous():
+            raise ValueError("weights must be contiguous float32 on the cache's GPU")
+        if t.shape != (self.pages, self.heads, self.page):
+            raise ValueError(f"weights must be [{self.pages}, {self.heads}, {self.page}]")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("weights require a gradient, which the cache's operators have not: call under torch.no_grad()")
+        return t.data_ptr()
+
     def _rows(self, t, heads, name):
         """t as rows that the kernels can take (a copy where its strides or
         alignment do not let them), its ltc_cache_rows as bytes and its shape."""
         if t.dtype is not self.dtype or t.get_device() != self._index:
             raise ValueError(f"{name} must be {self.dtype} on the cache's GPU")
-        if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{name} requires a gradient, which the cache's operators have not: call under torch.no_grad()")
-        shape = t.shape
-        if len(shape) != 3 or shape[2] != self.dim or (heads is not None and shape[1] != heads):
-            raise ValueError(f"{name} must be [rows, {'heads' if heads is None else heads}, {self.dim}]")
-        r, h, d = t.stride()
-        at = t.data_ptr()
-        if d != 1 or r % 8 or h % 8 or at % 16:
-            # a plain clone keeps the strides of dimensions of one, whatever they are
-            t = t.clone(memory_format=torch.contiguous_format)
-            r, h, d = t.stride()
-            at = t.data_ptr()
-        return t, _pack_rows(at, r, h), shape
+        return _take_rows(t, heads, self.dim, name)
 
 
 def cache_write(cache, k, v, table, lengths, cu=None):
@@ -229,23 +249,39 @@ def cache_read(cache, table, lengths, cu=None, rows=None):
     return k, v
 
 
-def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None):
+def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None, weights=None):
     """softmax(scale * q k^T) v of queries [rows, q_heads, dim] over the
     positions up to each row's own (with window: the last `window` of them);
     zeros for a row that sees nothing.  scale is dim^-0.5 by default.  A call
     is planned for sequences of about its mean: a prompt, or a context of many
-    times the others' length, is faster in a call of its own."""
+    times the others' length, is faster in a call of its own.
+
+    weights (float32 [pages, heads, page], as KVCache.no_weights() makes them)
+    get what each position is worth to the call's rows added to them: at its
+    token's place and each of the cache's heads, the softmax's weights of all
+    rows that see it and all query heads that read the head.  Those of the
+    positions that the rows stand for begin at zero.  No two sequences of such a
+    call may share a page."""
     if _current_gpu() != cache._index:
         with torch.cuda.device(cache._index):
-            return cache_attend(cache, q, table, lengths, cu, window, scale)
+            return cache_attend(cache, q, table, lengths, cu, window, scale, weights)
     if not 0 <= window < 1 << 31:  # ctypes would take it modulo 2^32
         raise LTCError(-1, f"window {window}")
     q, qr, (rows, q_heads, dim) = cache._rows(q, None, "q")
     s = cache._seqs(table, lengths, cu, rows)
     out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
     stream = _raw_stream(cache._index)
-    need = cache._lib.ltc_cache_attend_workspace_size(cache._ref, s, q_heads, window)
     scale = dim ** -0.5 if scale is None else scale
+    if weights is not None:
+        at = cache._weights(weights)
+        need = cache._lib.ltc_cache_attend_weigh_workspace_size(cache._ref, s, q_heads, window)
+        with cache._lock:
+            ws = cache._workspace(need, stream) if need else None
+            _check(cache._lib.ltc_cache_attend_weigh(cache._ref, s, qr, q_heads, window, scale, out.data_ptr(), at,
+                                                     ws.data_ptr() if need else None, ws.numel() if need else 0, stream),
+                   "cache_attend")
+        return out
+    need = cache._lib.ltc_cache_attend_workspace_size(cache._ref, s, q_heads, window)
     if not need:
         _check(cache._lib.ltc_cache_attend(cache._ref, s, qr, q_heads, window, scale, out.data_ptr(), None, 0, stream),
                "cache_attend")
@@ -257,3 +293,41 @@ def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None):
         _check(cache._lib.ltc_cache_attend(cache._ref, s, qr, q_heads, window, scale, out.data_ptr(), ws.data_ptr(),
                                            ws.numel(), stream), "cache_attend")
     return out
+
+
+def cache_evict(cache, weights, table, lengths, to, keep, recent=0):
+    """Cuts sequences to `keep` positions: the last `recent` ones, and of the
+    others those of most weight (of equal ones the first; a NaN is below all
+    numbers), each of the cache's heads by itself.  They are moved, in their
+    order and with their weights, to the pages that to [sequences, at least
+    keep / page] names, whose positions they are from then on: 0 to keep - 1.
+    Pages of `to` must not be in use, here or twice; those of table are free
+    afterwards.  A sequence of no more than `keep` positions keeps all of them.
+    4-bit codes are moved as they are; a page of 8-bit ones gets the largest
+    scale that its tokens had, and codes of smaller scales are rounded again.
+
+    Returns the new lengths, int32 [sequences], and the kept positions, int32
+    [sequences, heads, keep], in order and -1 behind the last."""
+    if _current_gpu() != cache._index:
+        with torch.cuda.device(cache._index):
+            return cache_evict(cache, weights, table, lengths, to, keep, recent)
+    if not 1 <= keep < 1 << 31 or not 0 <= recent <= keep:  # ctypes would take them modulo 2^32
+        raise LTCError(-1, f"keep {keep}, recent {recent}")
+    at, seqs = cache._weights(weights), lengths.numel()
+    s = cache._seqs(table, lengths, None, seqs)
+    if to.dtype is not _INT32 or to.get_device() != cache._index:
+        raise ValueError("to must be int32 on the cache's GPU")
+    pages = -(-keep // cache.page)
+    if to.dim() != 2 or to.shape[0] != seqs or to.shape[1] < pages:
+        raise ValueError(f"to must be [sequences, at least {pages} pages]")
+    width = to.shape[1]
+    if to.stride(1) != 1 and width > 1:
+        raise ValueError("the rows of to must be contiguous")
+    step = to.stride(0) if seqs > 1 else width
+    if step < width:
+        raise ValueError("the rows of to must not overlap")
+    new = torch.empty(seqs, dtype=_INT32, device=cache.device)
+    positions = torch.empty((seqs, cache.heads, keep), dtype=_INT32, device=cache.device)
+    _check(cache._lib.ltc_cache_evict(cache._ref, s, at, to.data_ptr(), step, width, keep, recent, new.data_ptr(),
+                                      positions.data_ptr(), _raw_stream(cache._index)), "cache_evict")
+    return new, positions

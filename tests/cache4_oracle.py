@@ -145,8 +145,9 @@ def attend(gather, heads, dim, page, q, table, lengths, cu=None, window=0, scale
         with it, and 2^-22 for exp2;
       sums over n positions in fp32: n 2^-24 of the sum of magnitudes, above
         and below the fraction.
-    A share has the errors of s and of the sum below its fraction, and its own
-    sum's over the rows."""
+    A share has the errors of s and of the sum below its fraction, its own
+    sum's over the rows, and for each row and query head 2^-126: below that, fp32's
+    smallest normal number, the result of exp2 is 0."""
     rows, HQ = q.shape[:2]
     G = HQ // heads
     scale = dim ** -0.5 if scale is None else scale
@@ -187,7 +188,7 @@ def attend(gather, heads, dim, page, q, table, lengths, cu=None, window=0, scale
                     slack[r0 + r, h] = 1.01 * (err * mean + floor)
                     got[h // G, seen] += share
                     off[h // G, seen] += 1.01 * share * (2 * exp_err + 2 * m * 2.0 ** -24)
-        off += got * (n * G + 2) * 2.0 ** -24
+        off += got * (n * G + 2) * 2.0 ** -24 + n * G * 2.0 ** -126
     return out, slack, shares, share_slack, status
 
 
