@@ -559,9 +559,10 @@ int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, c
                            uint32_t window, float scale, void* d_out, float* d_weights, void* d_ws, uint64_t ws_nbytes,
                            hipStream_t stream);
 
+uint64_t ltc_cache_evict_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs);
 int ltc_cache_evict(const ltc_cache* cache, const ltc_cache_seqs* seqs, float* d_weights, const int32_t* d_to,
                     uint64_t to_stride, uint32_t to_width, uint32_t keep, uint32_t recent, int32_t* d_lengths,
-                    int32_t* d_positions, hipStream_t stream);
+                    int32_t* d_positions, void* d_ws, uint64_t ws_nbytes, hipStream_t stream);
 
 typedef struct {
   const uint64_t* d_turns;

@@ -188,9 +188,17 @@ int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, c
   return launched(e);
 }
 
+uint64_t ltc_cache_evict_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs) {
+  CacheView c;
+  SeqView s;
+  if (check_cache(cache, &c) || check_seqs(seqs, &s)) return 0;
+  const uint64_t need = cache_evict_workspace(c, s);
+  return need ? LTC_CACHE_WS_ZEROS + need : 0;
+}
+
 int ltc_cache_evict(const ltc_cache* cache, const ltc_cache_seqs* seqs, float* d_weights, const int32_t* d_to,
                     uint64_t to_stride, uint32_t to_width, uint32_t keep, uint32_t recent, int32_t* d_lengths,
-                    int32_t* d_positions, hipStream_t stream) {
+                    int32_t* d_positions, void* d_ws, uint64_t ws_nbytes, hipStream_t stream) {
   CacheView c;
   SeqView s;
   int rc = check_cache(cache, &c);
@@ -201,9 +209,13 @@ int ltc_cache_evict(const ltc_cache* cache, const ltc_cache_seqs* seqs, float* d
   if (!keep || recent > keep || pages > kMaxEvictPages || to_width < pages || to_stride < to_width)
     return LTC_ERR_INVALID_ARGUMENT;
   if (!s.seqs) return LTC_OK;
-  if ((c.pages && !aligned(d_weights, 4)) || !aligned(d_to, 4) || !aligned(d_lengths, 4) || !aligned(d_positions, 4))
+  if ((c.pages && !aligned(d_weights, 16)) || !aligned(d_to, 4) || !aligned(d_lengths, 4) || !aligned(d_positions, 4))
     return LTC_ERR_INVALID_ARGUMENT;
-  const EvictArgs a = {d_weights, d_to, to_stride, keep, recent, d_lengths, d_positions};
+  const uint64_t need = cache_evict_workspace(c, s);
+  if (need && (ws_nbytes < LTC_CACHE_WS_ZEROS + need || !aligned(d_ws, 256))) return LTC_ERR_WORKSPACE;
+  // behind the bytes that calls leave zero
+  uint32_t* ws = need ? reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(d_ws) + LTC_CACHE_WS_ZEROS) : nullptr;
+  const EvictArgs a = {d_weights, d_to, to_stride, keep, recent, d_lengths, d_positions, ws};
   return launched(launch_cache_evict(c, s, cache->codes, a, stream));
 }
 

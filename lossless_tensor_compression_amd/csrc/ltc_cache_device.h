@@ -138,6 +138,12 @@ template <int BYTES> __device__ __forceinline__ uint32_t load_drops(const uint8_
   else return *at;
 }
 
+template <int BYTES> __device__ __forceinline__ void store_drops(uint8_t* at, uint32_t drops) {
+  if constexpr (BYTES == 4) *reinterpret_cast<uint32_t*>(at) = drops;
+  else if constexpr (BYTES == 2) *reinterpret_cast<uint16_t*>(at) = (uint16_t)drops;
+  else *at = (uint8_t)drops;
+}
+
 __device__ __forceinline__ void report(const CacheView& c, uint32_t bit) { atomicOr(c.status, bit); }
 
 // ---- on the host

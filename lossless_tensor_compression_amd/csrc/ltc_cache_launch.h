@@ -52,7 +52,10 @@ struct EvictArgs {
   uint64_t to_stride;
   uint32_t keep, recent;
   int32_t *lengths, *positions;
+  uint32_t* ws;
 };
+
+uint64_t cache_evict_workspace(const CacheView& c, const SeqView& s);
 
 hipError_t launch_cache_evict(const CacheView& c, const SeqView& s, int codes, const EvictArgs& a, hipStream_t st);
 

@@ -47,12 +47,6 @@ __device__ __forceinline__ uint32_t nibble_mask(int t, int lo, int hi) {
   return below_b & ~below_a;
 }
 
-__device__ __forceinline__ void store_drops(uint8_t* at, int bytes, uint32_t drops) {
-  if (bytes == 4) *reinterpret_cast<uint32_t*>(at) = drops;
-  else if (bytes == 2) *reinterpret_cast<uint16_t*>(at) = (uint16_t)drops;
-  else *at = (uint8_t)drops;
-}
-
 template <int DT, int D>
 __global__ __launch_bounds__(1024) void k_cache4_write(CacheView c, SeqView s, UnitMap map, RowsView k, RowsView v) {
   using S = Share<D>;
@@ -138,7 +132,7 @@ __global__ __launch_bounds__(1024) void k_cache4_write(CacheView c, SeqView s, U
     drops |= (uint32_t)__shfl_xor((int)drops, 32);
     if (fresh && g == 0) {
       scales[kt] = (uint8_t)(e + 127);
-      store_drops(scales + 2 * P + kt * DROPS, DROPS, drops);
+      store_drops<DROPS>(scales + 2 * P + kt * DROPS, drops);
     }
   }
   // ---- values

@@ -328,6 +328,11 @@ def cache_evict(cache, weights, table, lengths, to, keep, recent=0):
         raise ValueError("the rows of to must not overlap")
     new = torch.empty(seqs, dtype=_INT32, device=cache.device)
     positions = torch.empty((seqs, cache.heads, keep), dtype=_INT32, device=cache.device)
-    _check(cache._lib.ltc_cache_evict(cache._ref, s, at, to.data_ptr(), step, width, keep, recent, new.data_ptr(),
-                                      positions.data_ptr(), _raw_stream(cache._index)), "cache_evict")
+    stream = _raw_stream(cache._index)
+    need = cache._lib.ltc_cache_evict_workspace_size(cache._ref, s)
+    with cache._lock:
+        ws = cache._workspace(need, stream) if need else None
+        _check(cache._lib.ltc_cache_evict(cache._ref, s, at, to.data_ptr(), step, width, keep, recent, new.data_ptr(),
+                                          positions.data_ptr(), ws.data_ptr() if need else None, ws.numel() if need else 0,
+                                          stream), "cache_evict")
     return new, positions

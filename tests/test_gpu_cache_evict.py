@@ -96,6 +96,25 @@ def test_ties_and_odd_weights(ltc, weights, codes, dtype, keep, recent):
     check(ltc, prepared(ltc, 72, 2, 64, 32, codes, dtype, [150, 1200, 90, 2500], keep, weights), keep, recent)
 
 
+def _few_hundreds(rng, shape):
+    return (rng.integers(0, 300, shape) / 300).astype(np.float32)
+
+
+@pytest.mark.parametrize("weights", [None, _ties, _odd, _few_hundreds, lambda rng, shape: np.ones(shape, np.float32)])
+@pytest.mark.parametrize("heads,lengths,keep,recent", [(2, [20001, 300, 8193, 1], 5000, 40), (1, [40000], 39999, 0),
+                                                       (3, [12345, 9000], 1, 0), (1, [33000], 700, 700), (1, [66000], 9000, 5)])
+def test_many_positions(ltc, heads, lengths, keep, recent, weights):
+    """Shared by several workgroups a sequence and head."""
+    banner(f"evict {lengths} to {keep}")
+    check(ltc, prepared(ltc, 79, heads, 64, 64, "e2m1", BF, lengths, keep, weights), keep, recent)
+
+
+@pytest.mark.parametrize("weights", [None, _few_hundreds])
+def test_many_positions_of_many_heads(ltc, weights):
+    """One workgroup a sequence and head, more positions than it holds."""
+    check(ltc, prepared(ltc, 80, 5, 64, 256, "int8", FP, [34000] + [1000 + 700 * i for i in range(13)], 2000, weights), 2000, 77)
+
+
 @pytest.mark.parametrize("codes", ["e4m3", "int8"])
 def test_scales_far_apart(ltc, codes):
     """8-bit pages of very different scales: codes are rounded to the largest one's."""
@@ -104,6 +123,18 @@ def test_scales_far_apart(ltc, codes):
     s.upload(ltc)
     s.gtable, s.glengths = torch.from_numpy(s.table).cuda(), torch.tensor(s.lengths, dtype=torch.int32, device="cuda")
     check(ltc, s, 70, 8)
+
+
+@pytest.mark.parametrize("codes", ["e2m1", "e4m3"])
+def test_the_cache_s_first_page(ltc, codes):
+    """Page 0 in the middle of a sequence, its first kept token the second of 16."""
+    s = prepared(ltc, 78, 2, 64, 16, codes, BF, [64], 48, lambda rng, shape: np.ones(shape, np.float32))
+    swap = {0: s.table[0, 1], s.table[0, 1]: 0}
+    s.table = np.vectorize(lambda p: swap.get(p, p))(s.table).astype(np.int32)
+    s.to = np.vectorize(lambda p: swap.get(p, p))(s.to).astype(np.int32)
+    s.gtable = torch.from_numpy(s.table).cuda()
+    s.w[s.table[0, 0], :, :15] = 0.0  # position 15, then all of page 0
+    check(ltc, s, 48, 0)
 
 
 @pytest.mark.parametrize("codes", ["e2m1", "int8"])
