@@ -54,25 +54,61 @@ __device__ __forceinline__ float sum_scattered(float (&v)[16], int n) {
   for (int w = 8; w; w >>= 1)
 #pragma unroll
     for (int j = 0; j < w; ++j) {
-      const float send = n & w ? v[j] : v[j + w], keep = n & w ? v[j + w] : v[j];
+      float x = v[j], y = v[j + w];
+      asm("" : "+v"(x), "+v"(y));  // two registers, not one array with a place to be found by comparisons
+      const float send = n & w ? x : y, keep = n & w ? y : x;
       v[j] = keep + __shfl_xor(send, w);
     }
   return v[0];
 }
 
-// A wave takes 64 positions of a sequence and head and goes over all rows that see
+// Waves for each SIMD that the kernel's registers are to leave room for.
+constexpr int weigh_occupancy(int D, bool share) { return D <= 128 ? share && D > 64 ? 2 : 3 : share ? 2 : 1; }
+
+// A step's keys as they lie in memory.
+template <int CODES, int D> struct RawKeys {
+  static constexpr bool kFour = CODES == LTC_E2M1;
+  static constexpr int KL = D / 64;
+  Keys4<kFour ? D : 32> four[4];
+  uint4v wide[4][kFour ? 1 : KL];
+  uint2v tail[4];
+  // the same, to the compiler other ones: what is made of them is not kept over a loop
+  __device__ __forceinline__ void forget() {
+    for (int b = 0; b < 4; ++b) {
+      if constexpr (kFour) {
+        for (int x = 0; x < D / 32; ++x) asm("" : "+v"(four[b].c[x]));
+      } else {
+        for (int j = 0; j < KL; ++j) asm("" : "+v"(wide[b][j]));
+        if constexpr (D % 64) asm("" : "+v"(tail[b]));
+      }
+    }
+  }
+  // product x's part of block b
+  template <int DT> __device__ __forceinline__ auto as(int b, int x, int g) const {
+    if constexpr (kFour) return codes_as<CODES, DT>(four[b].c[x], 0, four[b].scale(x, g));
+    else return x < 2 * KL ? codes_as<CODES, DT>(wide[b][x / 2][(x & 1) * 2], wide[b][x / 2][(x & 1) * 2 + 1], 1.0f)
+                           : codes_as<CODES, DT>(tail[b][0], tail[b][1], 1.0f);
+  }
+};
+
+// A wave takes 64 positions of a sequence and head and goes over rows that see
 // them, 16 packed rows at a time: the products are k_attend_rows's first ones, in
 // the cache's own type.  A lane holds the weights of 16 positions from one row,
 // 2^(x - lse), adds them up over the rows, and at the end 16 lanes' sums are
-// joined.  No two waves have a position in common, so the sums' order is fixed.
-template <int CODES, int DT, int D>
-__global__ __launch_bounds__(64 * kWaves) void k_weigh(CacheView c, SeqView s, AttendArgs a, float* weights, uint32_t splits,
-                                                       uint32_t per_head) {
+// joined.  The order of all sums is fixed.
+//
+// SHARE: a workgroup's waves have the same positions and share the rows out, for
+// prompts; else each wave has every W-th step, for few rows.
+template <int CODES, int DT, int D, bool SHARE, int W>
+__global__ __launch_bounds__(64 * W, weigh_occupancy(D, SHARE)) void k_weigh(CacheView c, SeqView s, AttendArgs a, float* weights, uint32_t splits,
+                                                  uint32_t per_head) {
   constexpr bool kFour = CODES == LTC_E2M1;
   constexpr int KS = D / 32, KL = D / 64;
   constexpr uint32_t kBlockBytes = kFour ? 8 * D : 16 * D;
   typedef decltype(codes_as<CODES, DT>(0, 0, 0.0f)) Eight;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  __shared__ float parts[SHARE ? W : 1][kStep];
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t head, seq, split;
   place(blockIdx.x + gridDim.x * blockIdx.y, c.heads, splits, per_head, &head, &seq, &split);
   if (head >= c.heads || seq >= s.seqs) return;
@@ -85,72 +121,121 @@ __global__ __launch_bounds__(64 * kWaves) void k_weigh(CacheView c, SeqView s, A
   const int32_t* table = s.table + seq * s.table_stride;
   const float f = fmaxf(a.scale * kLog2e * (kFour ? power_of_two(-kLift) : 1.0f), 0x1p-126f);
   const int kb = n >> 2;
-  for (int step = lo / kStep + (int)split * kWaves + wave; step * kStep < len; step += (int)splits * kWaves) {
-    const int t0 = step * kStep;
-    auto page_of = [&](int t) -> uint32_t { return t < len ? (uint32_t)table[(uint32_t)t >> c.page_log] : ~0u; };
-    const int tk = t0 + kb * 16, tv = t0 + g * 16;
-    const uint32_t k_page = page_of(tk), v_page = page_of(tv);
-    const bool have = v_page < c.pages;
-    const uint32_t kp = k_page < c.pages ? k_page : 0, vp = have ? v_page : 0;
+  const int by = SHARE ? (int)splits : (int)splits * W;  // steps from one of the wave's to the next
+  int step = lo / kStep + (SHARE ? (int)split : (int)split * W + wave);
+  auto page_of = [&](int t) -> uint32_t { return t < len ? (uint32_t)table[(uint32_t)t >> c.page_log] : ~0u; };
+  // a step's keys are loaded a step ahead, its pages two
+  RawKeys<CODES, D> raw;
+  uint4v exps = {0, 0, 0, 0};
+  uint32_t k_page = page_of(step * kStep + kb * 16), v_page = page_of(step * kStep + g * 16), now_page = ~0u;
+  auto load = [&](int at) {
+    const int tk = at * kStep + kb * 16, tv = at * kStep + g * 16;
+    const uint32_t kp = k_page < c.pages ? k_page : 0, vp = v_page < c.pages ? v_page : 0;
     const uint8_t* k = c.k + head_offset(c, kp, head) / (kFour ? 2 : 1) + (((uint32_t)tk & page_mask) >> 4) * kBlockBytes +
                        (n & 3) * 16;
-    Eight key[4][KS];
-    uint4v ke = {0, 0, 0, 0};
     if constexpr (kFour) {
       const uint8_t* drops = c.scales + token_scales(c, kp, head) + 2 * (page_mask + 1) +
                              (((uint32_t)tk & page_mask) + (n & 3)) * drop_bytes(D);
-      Keys4<D> kq[4];
-      for (int b = 0; b < 4; ++b) kq[b].load(k + b * 64, drops + 4 * b * drop_bytes(D), g);
-      ke = *reinterpret_cast<const uint4v*>(c.scales + token_scales(c, vp, head) + ((uint32_t)tv & page_mask));
-      for (int b = 0; b < 4; ++b)
-        for (int x = 0; x < KS; ++x) key[b][x] = codes_as<CODES, DT>(kq[b].c[x], 0, kq[b].scale(x, g));
+      for (int b = 0; b < 4; ++b) raw.four[b].load(k + b * 64, drops + 4 * b * drop_bytes(D), g);
+      exps = *reinterpret_cast<const uint4v*>(c.scales + token_scales(c, vp, head) + ((uint32_t)tv & page_mask));
     } else {
-      uint4v kr[4][KL];
-      uint2v kt[4];
       for (int b = 0; b < 4; ++b) {
-        for (int j = 0; j < KL; ++j) kr[b][j] = *reinterpret_cast<const uint4v*>(k + g * 256 + j * 1024 + b * 64);
-        if constexpr (D % 64) kt[b] = *reinterpret_cast<const uint2v*>(k + KL * 1024 + (g >> 1) * 256 + (g & 1) * 8 + b * 64);
+        for (int j = 0; j < KL; ++j) raw.wide[b][j] = *reinterpret_cast<const uint4v*>(k + g * 256 + j * 1024 + b * 64);
+        if constexpr (D % 64) raw.tail[b] = *reinterpret_cast<const uint2v*>(k + KL * 1024 + (g >> 1) * 256 + (g & 1) * 8 + b * 64);
       }
-      ke[0] = c.scales[((uint64_t)vp * c.heads + head) * 2];
-      for (int b = 0; b < 4; ++b)
-        for (int x = 0; x < KS; ++x)
-          key[b][x] = x < 2 * KL ? codes_as<CODES, DT>(kr[b][x / 2][(x & 1) * 2], kr[b][x / 2][(x & 1) * 2 + 1], 1.0f)
-                                 : codes_as<CODES, DT>(kt[b][0], kt[b][1], 1.0f);
+      exps[0] = c.scales[((uint64_t)vp * c.heads + head) * 2];
     }
+    now_page = v_page;
+    k_page = page_of((at + by) * kStep + kb * 16);
+    v_page = page_of((at + by) * kStep + g * 16);
+  };
+  if (step * kStep < len) load(step);
+  for (; step * kStep < len; step += by) {
+    const int t0 = step * kStep, tv = t0 + g * 16;
+    const uint32_t page = now_page;
+    const bool have = page < c.pages;
+    const int t = tv + n;  // whose weight the lane has in the end
+    float* at = weights + (((uint64_t)(have ? page : 0) * c.heads + head) << c.page_log) + ((uint32_t)t & page_mask);
+    const bool mine = t < len && have && (!SHARE || wave == 0);
+    const float before = mine && t < start ? *at : 0.0f;
+    // many rows: the keys are turned into numbers once; few: for each 16 rows again,
+    // which leaves registers for more waves
+    RawKeys<CODES, D> now = raw;
+    Eight key[SHARE ? 4 : 1][SHARE ? KS : 1];
+    if constexpr (SHARE)
+      for (int b = 0; b < 4; ++b)
+        for (int x = 0; x < KS; ++x) key[b][x] = now.template as<DT>(b, x, g);
+    // what a token's products are multiplied with: log2(e) scale times the keys' scale
+    float by_token[kFour ? 16 : 1];
+    if constexpr (kFour) {
+      for (int t = 0; t < 16; ++t) by_token[t] = fmaxf(__builtin_amdgcn_ldexpf(f, (int)(exps[t / 4] >> (8 * (t % 4)) & 0xff) - 127), 0x1p-126f);
+    } else {
+      by_token[0] = fmaxf(__builtin_amdgcn_ldexpf(f, (int)exps[0] - 127), 0x1p-126f);
+    }
+    if ((step + by) * kStep < len) load(step + by);
     float sum[16];
     for (int t = 0; t < 16; ++t) sum[t] = 0.0f;
     // the rows at positions from t0 on, and with a window before t0 + 63 + window
     const uint32_t ra = (t0 > start ? (uint32_t)(t0 - start) : 0) * G;
     const uint32_t rb = (window ? min(sp.n, (uint32_t)max((int64_t)t0 + 63 + window - start, (int64_t)0)) : sp.n) * G;
-    for (uint32_t r0 = ra; r0 < rb; r0 += 16) {
-      const uint32_t r = r0 + n;
-      const bool live = r < rb;
-      const uint32_t token = live ? r / G : 0, qh = head * G + (live ? r % G : 0);
-      const uint64_t row = sp.row0 + token;
-      const uint16_t* src = a.q.base + row * a.q.row_stride + (uint64_t)qh * a.q.head_stride;
-      Eight q[KS];
+    uint32_t r0 = ra + (SHARE ? 16 * wave : 0);
+    constexpr uint32_t R = SHARE ? 16 * W : 16;
+    // row r0 + n as token and query head, counted on
+    uint32_t token = (r0 + n) / G, qh = (r0 + n) % G;
+    const uint32_t token_by = R / G, qh_by = R % G;
+    Eight q[KS];
+    float lse = 0.0f;
+    auto load_row = [&] {
+      const uint64_t row = sp.row0 + min(token, sp.n - 1);
+      const uint16_t* src = a.q.base + row * a.q.row_stride + (uint64_t)(head * G + qh) * a.q.head_stride;
       for (int x = 0; x < KS; ++x) q[x] = *reinterpret_cast<const Eight*>(src + dim_of<CODES, D>(x, g));
-      const float lse = a.lse[row * a.q_heads + qh];
+      lse = a.lse[row * a.q_heads + head * G + qh];
+    };
+    if (r0 < rb) load_row();
+    for (; r0 < rb; r0 += R) {
+      if constexpr (!SHARE) now.forget();
       float4v st[4];
       for (int b = 0; b < 4; ++b) st[b] = float4v{0, 0, 0, 0};
 #pragma unroll
       for (int x = 0; x < KS; ++x)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) st[b] = product(key[b][x], q[x], st[b]);
-      const int hi = live ? start + (int)token + 1 : 0, low = window ? hi - window : 0;
+        for (int b = 0; b < 4; ++b) {
+          if constexpr (SHARE) st[b] = product(key[b][x], q[x], st[b]);
+          else st[b] = product(now.template as<DT>(b, x, g), q[x], st[b]);
+        }
+      const float less = lse;
+      // all rows see all of the step's positions, or masks are needed
+      const int first = start + (int)(r0 / G);
+      const bool edge = t0 + kStep > first + 1 || r0 + 16 > rb || window;
+      const int hi = r0 + n < rb ? start + (int)token + 1 : 0, low = window ? hi - window : 0;
+      token += token_by;
+      qh += qh_by;
+      if (qh >= G) {
+        qh -= G;
+        ++token;
+      }
+      if (r0 + R < rb) load_row();
       for (int b = 0; b < 4; ++b)
         for (int i = 0; i < 4; ++i) {
-          const int t = tv + 4 * b + i, e = (int)(kFour ? ke[b] >> (8 * i) & 0xff : ke[0]) - 127;
-          const float p = __builtin_amdgcn_exp2f(fmaf(__builtin_amdgcn_ldexpf(st[b][i], e), f, -lse));
-          sum[4 * b + i] += t < hi && t >= low ? p : 0.0f;
+          float p = __builtin_amdgcn_exp2f(fmaf(st[b][i], by_token[kFour ? 4 * b + i : 0], -less));
+          if (edge) {
+            const int t = tv + 4 * b + i;
+            p = t < hi && t >= low ? p : 0.0f;
+          }
+          sum[4 * b + i] += p;
         }
     }
-    const float w = sum_scattered(sum, n);
-    const int t = tv + n;
-    if (t < len && have) {
-      float* at = weights + (((uint64_t)v_page * c.heads + head) << c.page_log) + ((uint32_t)t & page_mask);
-      *at = (t < start ? *at : 0.0f) + w;
+    float w = sum_scattered(sum, n);
+    if constexpr (SHARE) {
+      parts[wave][lane] = w;
+      __syncthreads();
+      if (wave == 0) {
+        w = 0.0f;
+        for (int v = 0; v < W; ++v) w += parts[v][lane];
+      }
+      __syncthreads();
     }
+    if (mine) *at = before + w;
   }
 }
 
@@ -160,15 +245,22 @@ template <int CODES>
 hipError_t launch_weigh(const CacheView& c, const SeqView& s, int dtype, const AttendArgs& a, float* weights, hipStream_t st) {
   uint64_t longest = (uint64_t)s.width << c.page_log;
   if (longest > kMaxPositions) longest = kMaxPositions;
-  const uint64_t most = (longest + kStep * kWaves - 1) / (kStep * kWaves);
-  const uint64_t base = (uint64_t)s.seqs * c.heads, want = (1024 + base - 1) / base;
+  const uint64_t steps = (longest + kStep - 1) / kStep, base = (uint64_t)s.seqs * c.heads;
+  const uint64_t mean = ((uint64_t)s.rows * (a.q_heads / c.heads) + s.seqs - 1) / s.seqs;  // packed rows of a sequence and head
+  const bool share = mean > 64;
+  constexpr int kShareWaves = 8;
+  const uint64_t most = share ? steps : (steps + kWaves - 1) / kWaves, want = ((share ? 4096 : 1024) + base - 1) / base;
   const uint32_t splits = (uint32_t)(want < most ? want : most < 1 ? 1 : most);
-  const uint32_t share = chiplet_share(c.heads);
-  const uint32_t per_head = (s.seqs * splits + share - 1) / share * share;
+  const uint32_t apart = chiplet_share(c.heads);
+  const uint32_t per_head = (s.seqs * splits + apart - 1) / apart * apart;
   const uint64_t groups = (uint64_t)per_head * c.heads;
   const dim3 grid((uint32_t)(groups < kGridWidth ? groups : kGridWidth), (uint32_t)((groups + kGridWidth - 1) / kGridWidth));
   return for_numbers(dtype, c.dim, [&](auto type, auto dim) {
-    k_weigh<CODES, decltype(type)::value, decltype(dim)::value><<<grid, 64 * kWaves, 0, st>>>(c, s, a, weights, splits, per_head);
+    constexpr int DT = decltype(type)::value, D = decltype(dim)::value;
+    if (share)
+      k_weigh<CODES, DT, D, true, kShareWaves><<<grid, 64 * kShareWaves, 0, st>>>(c, s, a, weights, splits, per_head);
+    else
+      k_weigh<CODES, DT, D, false, kWaves><<<grid, 64 * kWaves, 0, st>>>(c, s, a, weights, splits, per_head);
   });
 }
 
