@@ -80,6 +80,47 @@ __device__ __forceinline__ half8 codes4_to_half(uint32_t c, float scale) {
 // the most, 0.5 is 2^-6 then, a normal fp16 number, and with 0 the top is 6,144.
 constexpr int kLift = 10;
 
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+
+// Eight codes as numbers of the cache's own type, exactly (E2M1: times scale).
+template <int CODES, int DT> __device__ __forceinline__ auto codes_as(uint32_t a, uint32_t b, float scale) {
+  if constexpr (DT == LTC_FP16) {
+    if constexpr (CODES == LTC_E2M1) return codes4_to_half(a, scale);
+    else return codes_to_half<CODES>(a, b);
+  } else {
+    union {
+      bf8 b8;
+      bf2v b2[4];
+      uint32_t u[4];
+    } r;
+    if constexpr (CODES == LTC_E2M1) {
+      r.b2[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 0);
+      r.b2[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 1);
+      r.b2[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 2);
+      r.b2[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 3);
+    } else if constexpr (CODES == LTC_E4M3) {
+      r.b2[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, 1.0f, false);
+      r.b2[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, 1.0f, true);
+      r.b2[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, 1.0f, false);
+      r.b2[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, 1.0f, true);
+    } else {
+      const float4v x = code_values<false>(a), y = code_values<false>(b);
+      r.u[0] = pack2<LTC_BF16>(x[0], x[1]);
+      r.u[1] = pack2<LTC_BF16>(x[2], x[3]);
+      r.u[2] = pack2<LTC_BF16>(y[0], y[1]);
+      r.u[3] = pack2<LTC_BF16>(y[2], y[3]);
+    }
+    return r.b8;
+  }
+}
+
+__device__ __forceinline__ float4v product(half8 a, half8 b, float4v c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float4v product(bf8 a, bf8 b, float4v c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
 // Which dims a lane's k-group g of a key's product x covers, eight from this one
 // on.  The lane's 16 bytes of keys are 16 dims of 8 bits, so two products, or 32 of
 // 4 bits, which share a scale: four; what is left of the dims goes in half and
@@ -118,7 +159,6 @@ template <int D> struct Keys4 {
     const int block = x < F ? x / 4 * 4 + g : x < F + H ? F + (g >> 1) : D / 32 - 1;
     return __builtin_bit_cast(float, ((uint32_t)(127 + kLift) - (drops >> (4 * block) & 15)) << 23);
   }
-  __device__ __forceinline__ half8 half(int x, int g) const { return codes4_to_half(c[x], scale(x, g)); }
 };
 
 // Whether any of four E4M3 codes is a NaN (0x7f or 0xff).
@@ -185,9 +225,11 @@ __device__ __forceinline__ float rebase(float l, float from, float to) {
 }
 
 // What a wave keeps of its 16 * NC rows; lane 16 g + n has row n of each 16.
-template <int D, int NC> struct Rows {
-  half8 q[NC][D / 32];     // the k-group g of the queries, times 2^up
-  int up[NC];
+// Eight: eight numbers as the first product takes them, fp16; bf16 from a bf16
+// cache of 4-bit codes.
+template <int D, int NC, class Eight = half8> struct Rows {
+  Eight q[NC][D / 32];     // the k-group g of the queries, times 2^up
+  int up[NC];              // 0 from a cache of 4-bit codes
   int lo[NC], hi[NC];      // the positions [lo, hi) that the row sees
   float4v acc[NC][D / 16]; // dims 16 i + 4 g + 0..3 of the numerator
   float m[NC], l[NC];      // bound, and the lane's part of the denominator
@@ -195,8 +237,8 @@ template <int D, int NC> struct Rows {
 };
 
 // Rows r0.. of a sequence and head; those from packed on are none, and see nothing.
-template <int CODES, int D, int NC>
-__device__ __forceinline__ void load_rows(Rows<D, NC>& w, const AttendArgs& a, const Span& sp, uint32_t head, uint32_t G,
+template <int CODES, int D, int NC, class Eight>
+__device__ __forceinline__ void load_rows(Rows<D, NC, Eight>& w, const AttendArgs& a, const Span& sp, uint32_t head, uint32_t G,
                                           uint32_t r0, uint32_t packed, bool bf16, int n, int g) {
   constexpr int KS = D / 32;
   for (int nc = 0; nc < NC; ++nc) {
@@ -211,7 +253,9 @@ __device__ __forceinline__ void load_rows(Rows<D, NC>& w, const AttendArgs& a, c
       raw[x] = live ? *reinterpret_cast<const uint4v*>(src + dim_of<CODES, D>(x, g)) : uint4v{0, 0, 0, 0};
     }
     w.up[nc] = 0;
-    if (bf16) {
+    if constexpr (CODES == LTC_E2M1) {
+      for (int x = 0; x < KS; ++x) w.q[nc][x] = __builtin_bit_cast(Eight, raw[x]);
+    } else if (bf16) {
       // to fp16 by a power of two that brings the row's largest number to
       // 2^14..2^15: what is lost is below 2^-39 of it, less than the sum's
       // own rounding in fp32
@@ -294,28 +338,46 @@ __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4
   }
 }
 
-// The same for tokens that have scales of their own: ke and ve are the bytes of
-// the lane's 16 tokens' exponents, and the keys' codes came times 2^(kLift - drop).
-// Everything is 127 higher than x + w: the byte stands for w.
-template <int D, int NC>
-__device__ __forceinline__ void step_weights4(Rows<D, NC>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], float base,
-                                              uint4v ke, uint4v ve, int tv, bool edge, bool have) {
-  const float f = fmaxf(base * power_of_two(-kLift), 0x1p-126f);  // not 0: hidden scores are -infinity
+// 4-bit codes: every token has scales of its own.  A lane makes of one token's
+// exponents what all lanes need, and finds that of its own 16 tokens in shared
+// memory: [0] log2(e) scale times the keys' scale, [1] w, [2] 2^(-w - kHead).
+struct Tokens4 {
+  float f[3][kStep];
+};
+__device__ __forceinline__ float key_factor(uint32_t byte, float f) { return f * power_of_two((int)byte - 127); }
+__device__ __forceinline__ float value_exponent(uint32_t byte) { return (float)((int)byte - 127); }
+__device__ __forceinline__ float value_inverse(uint32_t byte) { return power_of_two(127 - kHead - (int)byte); }
+
+// far: some token's w lies more than kSpread from a first one's, here or in a step
+// before.  Else every weight that counts below the fraction is one above it too.
+constexpr int kSpread = 30;
+
+// The products of a step to weights.
+template <int D, int NC, class Eight>
+__device__ __forceinline__ void step_weights4(Rows<D, NC, Eight>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], const Tokens4& of,
+                                              int tv, bool edge, bool have, bool far) {
+  const int own = tv & (kStep - 1);
+  float4v factor[4], wv[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    factor[b] = *reinterpret_cast<const float4v*>(&of.f[0][own + 4 * b]);
+    wv[b] = *reinterpret_cast<const float4v*>(&of.f[1][own + 4 * b]);
+  }
 #pragma unroll
   for (int nc = 0; nc < NC; ++nc) {
-    float top = -INFINITY;
     for (int b = 0; b < 4; ++b)
-      for (int i = 0; i < 4; ++i) {
-        const float wv = (float)(ve[b] >> (8 * i) & 0xff);
-        float x = __builtin_amdgcn_ldexpf(st[nc][b][i], (int)(ke[b] >> (8 * i) & 0xff) - 127 - w.up[nc]) * f;
-        if (edge) {
+      for (int i = 0; i < 4; ++i) st[nc][b][i] = fmaf(st[nc][b][i], factor[b][i], wv[b][i]);
+    if (edge) {
+      for (int b = 0; b < 4; ++b)
+        for (int i = 0; i < 4; ++i) {
           const int t = tv + 4 * b + i;
           const bool seen = t >= w.lo[nc] && t < w.hi[nc] && have;
-          x = seen ? x : -INFINITY;
+          st[nc][b][i] = seen ? st[nc][b][i] : -INFINITY;
         }
-        st[nc][b][i] = x;
-        top = fmaxf(top, x + wv);
-      }
+    }
+    float top = st[nc][0][0];
+    for (int b = 0; b < 4; ++b)
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, st[nc][b][i]);
     if (__any(top > fmaf(fabsf(w.m[nc]), -kFar, w.m[nc]) + kSlack)) {
       float now = fmaxf(top, __shfl_xor(top, 16));
       now = fmaxf(now, __shfl_xor(now, 32));
@@ -326,16 +388,24 @@ __device__ __forceinline__ void step_weights4(Rows<D, NC>& w, float4v (&st)[NC][
       for (int i = 0; i < D / 16; ++i) w.acc[nc][i] *= keep;
     }
     // nothing seen yet: every weight is 0
-    const float m = w.m[nc] == -INFINITY ? 0.0f : w.m[nc];
+    const float m = w.m[nc] == -INFINITY ? 0.0f : w.m[nc], shift = kHead - m;
+    if (far) {
+      // not the weight times 2^-w: that may be below fp32's numbers where this is not
+      float sum = 0.0f;
+      for (int b = 0; b < 4; ++b)
+        for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f((st[nc][b][i] - wv[b][i]) - m);
+      w.l[nc] += sum;
+    }
     float sum = 0.0f;
-    for (int b = 0; b < 4; ++b)
+    for (int b = 0; b < 4; ++b) {
+      const float4v inverse = *reinterpret_cast<const float4v*>(&of.f[2][own + 4 * b]);
       for (int i = 0; i < 4; ++i) {
-        const float wv = (float)(ve[b] >> (8 * i) & 0xff);
-        p[nc][b >> 1][(b & 1) * 4 + i] = (_Float16)__builtin_amdgcn_exp2f(st[nc][b][i] + (wv - m + kHead));
-        // not the weight times 2^-w: that may be below fp32's numbers where this is not
-        sum += __builtin_amdgcn_exp2f(st[nc][b][i] + (127.0f - m));
+        const float u = __builtin_amdgcn_exp2f(st[nc][b][i] + shift);
+        sum = fmaf(u, inverse[i], sum);
+        p[nc][b >> 1][(b & 1) * 4 + i] = (_Float16)u;
       }
-    w.l[nc] += sum;
+    }
+    if (!far) w.l[nc] += sum;
   }
 }
 
@@ -343,8 +413,8 @@ __device__ __forceinline__ void step_weights4(Rows<D, NC>& w, float4v (&st)[NC][
 // v + 256 i): the rows that see one take note of it, by a product of
 // indicators, so that the codes can lose it before they meet the weights of
 // rows that do not (0 * NaN is NaN).
-template <int D, int NC>
-__device__ __forceinline__ void note_nan(Rows<D, NC>& w, int tv, bool have, const uint8_t* v) {
+template <int D, int NC, class Eight>
+__device__ __forceinline__ void note_nan(Rows<D, NC, Eight>& w, int tv, bool have, const uint8_t* v) {
   asm volatile("" : "+v"(tv));  // nothing of this before the branch that leads here
   for (int nc = 0; nc < NC; ++nc) {
     half8 ind[2];
@@ -368,7 +438,7 @@ __device__ __forceinline__ void note_nan(Rows<D, NC>& w, int tv, bool have, cons
   }
 }
 
-template <int D, int NC> __device__ __forceinline__ void apply_nan(Rows<D, NC>& w) {
+template <int D, int NC, class Eight> __device__ __forceinline__ void apply_nan(Rows<D, NC, Eight>& w) {
   for (int nc = 0; nc < NC; ++nc)
     if (__any(w.nan[nc] != 0))
       for (int i = 0; i < D / 16; ++i)
@@ -392,7 +462,7 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, const Span& sp, u
     const bool small = below < 0x1p-100f;  // the logarithm takes no subnormal numbers
     const float log = small ? __builtin_amdgcn_logf(below * 0x1p64f) - 64.0f : __builtin_amdgcn_logf(below);
     a.lse[(uint64_t)(sp.row0 + token) * a.q_heads + qh] =
-        below == 0.0f ? -INFINITY : (CODES == LTC_E2M1 ? top - 127.0f : top) + log;
+        below == 0.0f ? -INFINITY : top + log;
   }
 }
 
@@ -450,13 +520,15 @@ constexpr int rows_occupancy(int D, int NC) { return D * NC <= 64 ? 3 : D * NC <
 // at 1,001-6,001 positions (8 heads of 128, 32 query heads) 93 us, 4.6 TB/s, one
 // at 131,071 58 us; by the chain lengths, table, codes, partial results, join
 // where there is not: one at 777 positions 9 us.
-template <int CODES, int D, int NC, int W>
+template <int CODES, int D, int NC, int W, bool BF>
 __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16, uint32_t units, uint32_t splits, uint32_t per_head) {
   constexpr int R = 16 * NC, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
   constexpr bool kFour = CODES == LTC_E2M1;
   constexpr uint32_t kBlockBytes = kFour ? 8 * D : 16 * D;  // of 16 tokens' keys or values
   constexpr int VL = kFour ? DB / 2 : DB;                   // 16 bytes of values: a dim, or two of 4 bits
+  typedef typename std::conditional<kFour && BF, bf8, half8>::type Eight;
+  __shared__ Tokens4 lds_tokens[kFour ? W : 1];
   __shared__ float lds_acc[W][16][D + 4];
   __shared__ float lds_m[W][R], lds_l[W][R];
   __shared__ bool lds_last;
@@ -486,7 +558,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   if ((int)split >= max(rg.used, 1)) return;
 
   const float base = a.scale * kLog2e;
-  Rows<D, NC> w;
+  Rows<D, NC, Eight> w;
   load_rows<CODES, D, NC>(w, a, sp, head, G, r0, packed, bf16, n, g);
   // positions that every row sees need no masks
   const int all_lo = a.window ? max((int)(sp.start + (r1 - 1) / G) + 1 - (int)a.window, 0) : 0;
@@ -509,7 +581,9 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   uint2v kt[4];
   Keys4<D> kq[4];
   uint32_t scales = 0;
-  uint4v exps[2] = {};  // the bytes of 16 tokens' exponents, keys and values
+  uint32_t exps[2] = {};  // the bytes of a token's exponents, key and value
+  int first_w = -1;       // the first one's
+  bool far = false;
   bool have_v, next_have_v = false;
   auto load_k = [&](uint64_t off, int t, int32_t page, bool have) {
     if constexpr (kFour) {
@@ -532,9 +606,9 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
   };
   auto load_scales = [&](int32_t p, int t, bool have) {
     if constexpr (kFour) {
-      const uint8_t* at = c.scales + token_scales(c, have ? (uint32_t)p : 0, head) + ((uint32_t)t & page_mask);
-      exps[0] = *reinterpret_cast<const uint4v*>(at);
-      exps[1] = *reinterpret_cast<const uint4v*>(at + page_mask + 1);
+      const uint8_t* at = c.scales + token_scales(c, have ? (uint32_t)p : 0, head) + ((uint32_t)t & page_mask) + n;
+      exps[0] = at[0];
+      exps[1] = at[page_mask + 1];
     } else {
       scales = *reinterpret_cast<const uint16_t*>(c.scales + ((uint64_t)(have ? (uint32_t)p : 0) * c.heads + head) * 2);
     }
@@ -559,7 +633,14 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     const int t0 = step * kStep, tv = t0 + g * 16;
     have_v = next_have_v;
     const uint32_t sc = scales;
-    const uint4v ke = exps[0], ve = exps[1];
+    if constexpr (kFour) {
+      Tokens4& to = lds_tokens[wave];
+      to.f[0][lane] = key_factor(exps[0], base * power_of_two(-kLift));
+      to.f[1][lane] = value_exponent(exps[1]);
+      to.f[2][lane] = value_inverse(exps[1]);
+      if (first_w < 0) first_w = __builtin_amdgcn_readfirstlane((int)exps[1]);
+      far = far || __any(abs((int)exps[1] - first_w) > kSpread);
+    }
     // ---- S^T
     float4v st[NC][4];
     for (int nc = 0; nc < NC; ++nc)
@@ -568,13 +649,12 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
-        half8 k8;
-        if constexpr (kFour) k8 = kq[b].half(x, g);
+        Eight k8;
+        if constexpr (kFour) k8 = codes_as<CODES, BF ? LTC_BF16 : LTC_FP16>(kq[b].c[x], 0, kq[b].scale(x, g));
         else if (x < 2 * KL) k8 = codes_to_half<CODES>(kr[b][x / 2][(x & 1) * 2], kr[b][x / 2][(x & 1) * 2 + 1]);
         else k8 = codes_to_half<CODES>(kt[b][0], kt[b][1]);
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-          st[nc][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w.q[nc][x], st[nc][b], 0, 0, 0);
+        for (int nc = 0; nc < NC; ++nc) st[nc][b] = product(k8, w.q[nc][x], st[nc][b]);
       }
     const int next = step + W;
     uint64_t next_v = v_off;
@@ -591,8 +671,17 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     if (lost && n == 0) report(c, kCacheBadPage);
     const bool edge = t0 < all_lo || t0 + kStep > all_hi || __any(lost);
     half8 p[NC][2];
-    if constexpr (kFour) step_weights4<D, NC>(w, st, p, base, ke, ve, tv, edge, have_v);
-    else step_weights<D, NC>(w, st, p, base, sc, tv, edge, have_v);
+    if constexpr (kFour) {
+      // written and read by one wave, whose accesses stay in order
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      step_weights4(w, st, p, lds_tokens[wave], tv, edge, have_v, far);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    } else {
+      step_weights<D, NC>(w, st, p, base, sc, tv, edge, have_v);
+    }
     // ---- O^T
     if (edge && !kFour) {
       // codes that no row sees may be anything, and 0 * NaN is NaN
@@ -605,7 +694,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
         for (int i = 0; i < DB; ++i)
           for (int dw = 0; dw < 4; ++dw) any |= nan_bytes(vr[i][dw]);
         if (__any(any != 0)) {
-          note_nan<D, NC>(w, tv, have_v, c.v + v_off + n * 16);
+          note_nan(w, tv, have_v, c.v + v_off + n * 16);
           for (int dw = 0; dw < 4; ++dw) {
             const uint32_t keep = have_v ? byte_mask(tv + 4 * dw, rg.lo, rg.hi) : 0;
             for (int i = 0; i < DB; ++i)
@@ -629,7 +718,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
     if (next < step_end) load_v(v_off);
   }
 
-  if constexpr (CODES == LTC_E4M3) apply_nan<D, NC>(w);
+  if constexpr (CODES == LTC_E4M3) apply_nan(w);
   // ---- the waves' parts together
   for (int nc = 0; nc < NC; ++nc) {
     w.l[nc] += __shfl_xor(w.l[nc], 16);
@@ -823,7 +912,7 @@ template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
 // turning 12% faster, without loads 14%, with an eighth of the second product
 // 10%: the chain of a step (read, product, maximum, exp2, product) is longer
 // than two waves a SIMD hide.
-template <int CODES, int D>
+template <int CODES, int D, bool BF>
 __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
                                                                           AttendArgs a, bool bf16, uint32_t units,
                                                                           uint32_t per_head) {
@@ -831,7 +920,9 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
   constexpr bool kFour = CODES == LTC_E2M1;
   constexpr uint32_t kBlockBytes = kFour ? 8 * D : 16 * D;
   constexpr int VB = kFour ? DB / 2 : DB, VL = (VB + 3) / 4;
+  typedef typename std::conditional<kFour && BF, bf8, half8>::type Eight;
   __shared__ half8 lds[2][(KS * 4 + DB * 2) * 64];  // keys [x][b][lane], values [i][h][lane]
+  __shared__ Tokens4 lds_tokens[kFour ? 2 : 1];
   __shared__ int lds_nan[2];                        // 1 + the step whose values have a NaN
   constexpr int kValues = KS * 4;
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
@@ -862,7 +953,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
   const bool live = w0 < w1 && rg.steps > 0;
   const int hi = live ? (int)(sp.start + (w1 - 1) / G) + 1 : 0, all_hi = live ? (int)(sp.start + w0 / G) + 1 : 0;
   const int lo = a.window ? max(all_hi - (int)a.window, 0) : 0, all_lo = a.window ? max(hi - (int)a.window, 0) : 0;
-  Rows<D, NC> w;
+  Rows<D, NC, Eight> w;
   load_rows<CODES, D, NC>(w, a, sp, head, G, w0, packed, bf16, n, g);
 
   const uint32_t page_mask = (1u << c.page_log) - 1;
@@ -878,7 +969,9 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
   uint4v kr[KL], vr[VL];
   uint2v kt = {0, 0};
   Keys4<D> kq;
-  uint4v exps[2] = {}, next_exps[2] = {};  // of the step computed, and of the next one, at g's tokens
+  uint32_t exps[2] = {};  // the bytes of a token's exponents, key and value, of the step to turn next
+  int first_w = -1;       // the first one's
+  bool far = false;
   int32_t k_page = -1, v_page = -1;           // of the step to load next
   int32_t page = -1, next_page = -1;          // of the step computed, and of the next one, at g's tokens
   uint32_t scales = 0, next_scales = 0;
@@ -894,8 +987,8 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
       const uint8_t* sk = c.scales + token_scales(c, (uint32_t)k_page < c.pages ? (uint32_t)k_page : 0, head);
       const uint8_t* sv = c.scales + token_scales(c, (uint32_t)v_page < c.pages ? (uint32_t)v_page : 0, head);
       kq.load(k, sk + 2 * (page_mask + 1) + (((uint32_t)tk & page_mask) + (n & 3) + 4 * wave) * drop_bytes(D), g);
-      next_exps[0] = *reinterpret_cast<const uint4v*>(sv + ((uint32_t)tv & page_mask));
-      next_exps[1] = *reinterpret_cast<const uint4v*>(sv + ((uint32_t)tv & page_mask) + page_mask + 1);
+      exps[0] = sv[((uint32_t)tv & page_mask) + n];
+      exps[1] = sv[((uint32_t)tv & page_mask) + n + page_mask + 1];
     } else {
       for (int j = 0; j < KL; ++j) kr[j] = *reinterpret_cast<const uint4v*>(k + g * 256 + j * 1024);
       if constexpr (TAIL) kt = *reinterpret_cast<const uint2v*>(k + KL * 1024 + (g >> 1) * 256 + (g & 1) * 8);
@@ -911,10 +1004,18 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
   auto turn = [&](int step) {
     half8* to = lds[step & 1] + lane;
     if constexpr (kFour) {
-      for (int x = 0; x < KS; ++x) to[(x * 4 + wave) * 64] = kq.half(x, g);
+      for (int x = 0; x < KS; ++x)
+        to[(x * 4 + wave) * 64] =
+            __builtin_bit_cast(half8, codes_as<CODES, BF ? LTC_BF16 : LTC_FP16>(kq.c[x], 0, kq.scale(x, g)));
       for (int i = 0; i < VL; ++i)
         if (VB % 4 == 0 || wave + 4 * i < VB)
           for (int h = 0; h < 4; ++h) to[(kValues + 4 * (wave + 4 * i) + h) * 64] = codes4_to_half(vr[i][h], 1.0f);
+      Tokens4& of = lds_tokens[step & 1];
+      if (wave == 0) of.f[0][lane] = key_factor(exps[0], base * power_of_two(-kLift));
+      if (wave == 1) of.f[1][lane] = value_exponent(exps[1]);
+      if (wave == 2) of.f[2][lane] = value_inverse(exps[1]);
+      if (first_w < 0) first_w = __builtin_amdgcn_readfirstlane((int)exps[1]);
+      far = far || __any(abs((int)exps[1] - first_w) > kSpread);  // a step early: no harm
       return;
     }
     for (int j = 0; j < KL; ++j)
@@ -956,7 +1057,6 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
     turn(step);
     page = next_page;
     scales = next_scales;
-    for (int i = 0; i < 2; ++i) exps[i] = next_exps[i];
     if (step + 1 < step_end) load(step + 1);
   }
   for (; step < step_end; ++step) {
@@ -964,12 +1064,10 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
     const int32_t p_now = page;
     const bool have = (uint32_t)p_now < c.pages;
     const uint32_t sc = scales;
-    const uint4v ke = exps[0], ve = exps[1];
     if (step + 1 < step_end) {
       turn(step + 1);
       page = next_page;
       scales = next_scales;
-      for (int i = 0; i < 2; ++i) exps[i] = next_exps[i];
       if (step + 2 < step_end) load(step + 2);
     }
     const int t0 = step * kStep, tv = t0 + g * 16;
@@ -983,10 +1081,9 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
     for (int x = 0; x < KS; ++x)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const half8 k8 = from[(x * 4 + b) * 64];
+        const Eight k8 = __builtin_bit_cast(Eight, from[(x * 4 + b) * 64]);
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc)
-          st[nc][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k8, w.q[nc][x], st[nc][b], 0, 0, 0);
+        for (int nc = 0; nc < NC; ++nc) st[nc][b] = product(k8, w.q[nc][x], st[nc][b]);
       }
     reads_ahead<KS, NC>();
     // ---- weights
@@ -994,7 +1091,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
     if (lost && n == 0) report(c, kCacheBadPage);
     const bool edge = t0 < all_lo || t0 + kStep > all_hi || __any(lost);
     half8 p[NC][2];
-    if constexpr (kFour) step_weights4<D, NC>(w, st, p, base, ke, ve, tv, edge, have);
+    if constexpr (kFour) step_weights4(w, st, p, lds_tokens[step & 1], tv, edge, have, far);
     else step_weights<D, NC>(w, st, p, base, sc, tv, edge, have);
     // ---- O^T
     from += kValues * 64;
@@ -1010,9 +1107,9 @@ __global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheV
             w.acc[nc][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p[nc][h], w.acc[nc][j], 0, 0, 0);
         }
     reads_ahead<DB / 2, NC>();
-    if (CODES == LTC_E4M3 && lds_nan[step & 1] == step + 1) note_nan<D, NC>(w, tv, have, c.v + block_at(tv, p_now) + n * 16);
+    if (CODES == LTC_E4M3 && lds_nan[step & 1] == step + 1) note_nan(w, tv, have, c.v + block_at(tv, p_now) + n * 16);
   }
-  if constexpr (CODES == LTC_E4M3) apply_nan<D, NC>(w);
+  if constexpr (CODES == LTC_E4M3) apply_nan(w);
   for (int nc = 0; nc < NC; ++nc) {
     float below = w.l[nc];
     below += __shfl_xor(below, 16);
@@ -1084,22 +1181,22 @@ inline Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, ui
   return p;
 }
 
-template <int CODES, int D, int W>
+template <int CODES, int D, int W, bool BF>
 hipError_t launch_waves(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
                         hipStream_t st) {
   auto launch = [&](auto kernel) {
     kernel<<<p.grid, 64 * W, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
   };
-  if (p.nc == 1) launch(k_attend_rows<CODES, D, 1, W>);
-  else if constexpr (D <= 192) launch(k_attend_rows<CODES, D, 2, W>);
+  if (p.nc == 1) launch(k_attend_rows<CODES, D, 1, W, BF>);
+  else if constexpr (D <= 192) launch(k_attend_rows<CODES, D, 2, W, BF>);
   return hipGetLastError();
 }
 
-template <int CODES, int D>
+template <int CODES, int D, bool BF>
 hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
                        hipStream_t st) {
   if (p.tiles) {
-    k_attend_tiles<CODES, D><<<p.grid, 256, 0, st>>>(c, s, p.map, a, bf16, p.units, p.per_head);
+    k_attend_tiles<CODES, D, BF><<<p.grid, 256, 0, st>>>(c, s, p.map, a, bf16, p.units, p.per_head);
     return hipGetLastError();
   }
   // Heads of 192 and 256 dims leave a SIMD one wave: where nothing is split, two
@@ -1108,24 +1205,32 @@ hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const At
   // 143 / 176 us, 64 at 1,000-6,000 194 / 192 us.  With 128 dims: 62 / 72 us and
   // 113 / 92 us, so four there.
   if constexpr (D >= 192) {
-    if (p.splits == 1) return launch_waves<CODES, D, 2>(c, s, bf16, a, p, st);
+    if (p.splits == 1) return launch_waves<CODES, D, 2, BF>(c, s, bf16, a, p, st);
   }
-  return launch_waves<CODES, D, kWaves>(c, s, bf16, a, p, st);
+  return launch_waves<CODES, D, kWaves, BF>(c, s, bf16, a, p, st);
 }
 
 }  // namespace
 
-template <int CODES>
-hipError_t launch_attend(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, hipStream_t st) {
+template <int CODES, bool BF>
+hipError_t launch_dim(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, hipStream_t st) {
   const Plan p = plan_rows(c, s, a.q_heads, a.window);
   switch (c.dim) {
-    case 64: return launch_rows<CODES, 64>(c, s, bf16, a, p, st);
-    case 96: return launch_rows<CODES, 96>(c, s, bf16, a, p, st);
-    case 128: return launch_rows<CODES, 128>(c, s, bf16, a, p, st);
-    case 192: return launch_rows<CODES, 192>(c, s, bf16, a, p, st);
-    case 256: return launch_rows<CODES, 256>(c, s, bf16, a, p, st);
+    case 64: return launch_rows<CODES, 64, BF>(c, s, bf16, a, p, st);
+    case 96: return launch_rows<CODES, 96, BF>(c, s, bf16, a, p, st);
+    case 128: return launch_rows<CODES, 128, BF>(c, s, bf16, a, p, st);
+    case 192: return launch_rows<CODES, 192, BF>(c, s, bf16, a, p, st);
+    case 256: return launch_rows<CODES, 256, BF>(c, s, bf16, a, p, st);
   }
   return hipErrorInvalidValue;
+}
+
+// 4-bit codes: kernels for each type of the queries; of 8 bits they are the same.
+template <int CODES>
+hipError_t launch_attend(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, hipStream_t st) {
+  if constexpr (CODES == LTC_E2M1)
+    if (bf16) return launch_dim<CODES, true>(c, s, bf16, a, st);
+  return launch_dim<CODES, false>(c, s, bf16, a, st);
 }
 
 }  // namespace ltc

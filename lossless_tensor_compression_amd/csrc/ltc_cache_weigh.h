@@ -7,47 +7,6 @@
 namespace ltc {
 namespace {
 
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-
-// Eight codes as numbers of the cache's own type, exactly (E2M1: times scale).
-template <int CODES, int DT> __device__ __forceinline__ auto codes_as(uint32_t a, uint32_t b, float scale) {
-  if constexpr (DT == LTC_FP16) {
-    if constexpr (CODES == LTC_E2M1) return codes4_to_half(a, scale);
-    else return codes_to_half<CODES>(a, b);
-  } else {
-    union {
-      bf8 b8;
-      bf2v b2[4];
-      uint32_t u[4];
-    } r;
-    if constexpr (CODES == LTC_E2M1) {
-      r.b2[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 0);
-      r.b2[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 1);
-      r.b2[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 2);
-      r.b2[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 3);
-    } else if constexpr (CODES == LTC_E4M3) {
-      r.b2[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, 1.0f, false);
-      r.b2[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, 1.0f, true);
-      r.b2[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, 1.0f, false);
-      r.b2[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, 1.0f, true);
-    } else {
-      const float4v x = code_values<false>(a), y = code_values<false>(b);
-      r.u[0] = pack2<LTC_BF16>(x[0], x[1]);
-      r.u[1] = pack2<LTC_BF16>(x[2], x[3]);
-      r.u[2] = pack2<LTC_BF16>(y[0], y[1]);
-      r.u[3] = pack2<LTC_BF16>(y[2], y[3]);
-    }
-    return r.b8;
-  }
-}
-
-__device__ __forceinline__ float4v product(half8 a, half8 b, float4v c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ float4v product(bf8 a, bf8 b, float4v c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
 // The sums of v[t] over the 16 lanes n of a lane row; lane n gets that of t = n.
 __device__ __forceinline__ float sum_scattered(float (&v)[16], int n) {
 #pragma unroll
@@ -63,7 +22,7 @@ __device__ __forceinline__ float sum_scattered(float (&v)[16], int n) {
 }
 
 // Waves for each SIMD that the kernel's registers are to leave room for.
-constexpr int weigh_occupancy(int D, bool share) { return D <= 128 ? share && D > 64 ? 2 : 3 : share ? 2 : 1; }
+constexpr int weigh_occupancy(int D, bool share) { return D <= 128 ? share && D > 64 ? 2 : 3 : D <= 192 || !share ? 2 : 1; }
 
 // A step's keys as they lie in memory.
 template <int CODES, int D> struct RawKeys {
@@ -248,7 +207,6 @@ hipError_t launch_weigh(const CacheView& c, const SeqView& s, int dtype, const A
   const uint64_t steps = (longest + kStep - 1) / kStep, base = (uint64_t)s.seqs * c.heads;
   const uint64_t mean = ((uint64_t)s.rows * (a.q_heads / c.heads) + s.seqs - 1) / s.seqs;  // packed rows of a sequence and head
   const bool share = mean > 64;
-  constexpr int kShareWaves = 8;
   const uint64_t most = share ? steps : (steps + kWaves - 1) / kWaves, want = ((share ? 4096 : 1024) + base - 1) / base;
   const uint32_t splits = (uint32_t)(want < most ? want : most < 1 ? 1 : most);
   const uint32_t apart = chiplet_share(c.heads);
@@ -257,6 +215,7 @@ hipError_t launch_weigh(const CacheView& c, const SeqView& s, int dtype, const A
   const dim3 grid((uint32_t)(groups < kGridWidth ? groups : kGridWidth), (uint32_t)((groups + kGridWidth - 1) / kGridWidth));
   return for_numbers(dtype, c.dim, [&](auto type, auto dim) {
     constexpr int DT = decltype(type)::value, D = decltype(dim)::value;
+    constexpr int kShareWaves = D <= 192 ? 8 : 4;
     if (share)
       k_weigh<CODES, DT, D, true, kShareWaves><<<grid, 64 * kShareWaves, 0, st>>>(c, s, a, weights, splits, per_head);
     else
