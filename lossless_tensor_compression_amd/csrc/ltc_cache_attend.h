@@ -499,7 +499,9 @@ __device__ __forceinline__ void spoil_rows(const CacheView& c, const AttendArgs&
 // us, one at 131,071 57 -> 61 us; 2 instead of 1 for 192 dims: 170 -> 207 us.  The
 // most that go without spills else, but for 3 registers of E4M3's two blocks of
 // 128 dims.
-constexpr int rows_occupancy(int D, int NC) { return D * NC <= 64 ? 3 : D * NC <= 256 && D < 192 ? 2 : 1; }
+constexpr int rows_occupancy(int D, int NC, bool four) {
+  return D * NC <= 64 ? 3 : D * NC <= 256 && (four || D < 192) ? 2 : 1;
+}
 
 // W waves on a tile of 16 * NC packed rows (row r of a sequence and key head
 // is token r / G, query head r % G of the head's G) and one split of its
@@ -521,7 +523,7 @@ constexpr int rows_occupancy(int D, int NC) { return D * NC <= 64 ? 3 : D * NC <
 // at 131,071 58 us; by the chain lengths, table, codes, partial results, join
 // where there is not: one at 777 positions 9 us.
 template <int CODES, int D, int NC, int W, bool BF>
-__global__ __launch_bounds__(64 * W, rows_occupancy(D, NC)) void k_attend_rows(
+__global__ __launch_bounds__(64 * W, rows_occupancy(D, NC, CODES == LTC_E2M1)) void k_attend_rows(
     CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16, uint32_t units, uint32_t splits, uint32_t per_head) {
   constexpr int R = 16 * NC, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
   constexpr bool kFour = CODES == LTC_E2M1;
@@ -886,7 +888,7 @@ constexpr uint32_t kTileRows = 128;
 // Workgroups on a CU: as many as registers and shared memory hold.  3 instead
 // of 2 for one prompt of 4,096 rows of 64 dims: 142 -> 115 us; for 2,048 rows of
 // 96 dims registers spill: 64 -> 94 us (for E4M3's 64 dims one does).
-constexpr int tiles_occupancy(int D) { return D <= 64 ? 3 : D <= 128 ? 2 : 1; }
+constexpr int tiles_occupancy(int D, bool four) { return D <= 64 && !four ? 3 : D <= 128 ? 2 : 1; }
 
 // The order of a run of 4 * N reads of shared memory and their 4 * N * NC
 // products: always four reads ahead.
@@ -913,7 +915,7 @@ template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
 // 10%: the chain of a step (read, product, maximum, exp2, product) is longer
 // than two waves a SIMD hide.
 template <int CODES, int D, bool BF>
-__global__ __launch_bounds__(256, tiles_occupancy(D)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
+__global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
                                                                           AttendArgs a, bool bf16, uint32_t units,
                                                                           uint32_t per_head) {
   constexpr int NC = 2, WR = 16 * NC, R = kTileRows, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
@@ -1136,7 +1138,7 @@ constexpr int kWaves = 4;
 // one.  One row at 131,071 positions (D = 128) with 256 / 512 / 768 / 1024 of
 // them: 64 / 61 / 67 / 75 us; 16 sequences of 5 rows: 39 / 29 / 39 / 41 us; four
 // rows at 20,001 positions of 2 heads of 256 dims with 256 / 512: 46 / 78 us.
-constexpr uint32_t fill(int D, int NC) { return 256 * (rows_occupancy(D, NC) < 2 ? 1 : 2); }
+constexpr uint32_t fill(int D, int NC, bool four) { return 256 * (rows_occupancy(D, NC, four) < 2 ? 1 : 2); }
 constexpr uint32_t kGridWidth = 1u << 20;  // times a workgroup's lanes below 2^32
 
 struct Plan {
@@ -1147,7 +1149,7 @@ struct Plan {
   dim3 grid;
 };
 
-inline Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
+inline Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window, bool four) {
   Plan p;
   const uint32_t G = q_heads / c.heads;
   const uint64_t mean = ((uint64_t)s.rows * G + s.seqs - 1) / s.seqs;  // packed rows of a sequence and head
@@ -1171,7 +1173,7 @@ inline Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, ui
   if (window && window + 64 < longest) longest = window + 64;
   const uint64_t most = (longest + kStep * kWaves - 1) / (kStep * kWaves);
   const uint64_t base = (uint64_t)p.units * c.heads;
-  const uint64_t want = (fill((int)c.dim, (int)p.nc) + base - 1) / base;
+  const uint64_t want = (fill((int)c.dim, (int)p.nc, four) + base - 1) / base;
   p.splits = (uint32_t)(want < most ? want : most);
   if (p.splits < 1 || base > kCounters || p.tiles) p.splits = 1;
   const uint32_t share = chiplet_share(c.heads);
@@ -1204,7 +1206,7 @@ hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const At
   // 9 prompts of 33-517 rows of 256 dims 47 / 65 us, 300 rows at 10-900 positions
   // 143 / 176 us, 64 at 1,000-6,000 194 / 192 us.  With 128 dims: 62 / 72 us and
   // 113 / 92 us, so four there.
-  if constexpr (D >= 192) {
+  if constexpr (D >= 192 && CODES != LTC_E2M1) {
     if (p.splits == 1) return launch_waves<CODES, D, 2, BF>(c, s, bf16, a, p, st);
   }
   return launch_waves<CODES, D, kWaves, BF>(c, s, bf16, a, p, st);
@@ -1214,7 +1216,7 @@ hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const At
 
 template <int CODES, bool BF>
 hipError_t launch_dim(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, hipStream_t st) {
-  const Plan p = plan_rows(c, s, a.q_heads, a.window);
+  const Plan p = plan_rows(c, s, a.q_heads, a.window, CODES == LTC_E2M1);
   switch (c.dim) {
     case 64: return launch_rows<CODES, 64, BF>(c, s, bf16, a, p, st);
     case 96: return launch_rows<CODES, 96, BF>(c, s, bf16, a, p, st);

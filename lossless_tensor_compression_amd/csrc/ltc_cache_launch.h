@@ -36,7 +36,7 @@ struct AttendArgs {
   float* lse;  // [rows][q_heads] log2 of the softmax's sum, or null
 };
 
-uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window);
+uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window);
 
 hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, int codes, int dtype, const AttendArgs& a,
                                hipStream_t st);
