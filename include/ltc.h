@@ -571,9 +571,17 @@ typedef struct {
   uint32_t reserved;
 } ltc_rotation;
 
-int ltc_norm_rotate(const ltc_rotation* rotation, const ltc_cache_seqs* seqs, int dtype, const ltc_cache_rows* q,
-                    uint32_t q_heads, const void* d_q_weight, const ltc_cache_rows* k, uint32_t k_heads,
-                    const void* d_k_weight, float eps, void* d_q_out, void* d_k_out, hipStream_t stream);
+typedef struct {
+  ltc_cache_rows q, k;
+  const void *d_q_weight, *d_k_weight;
+  void *d_q_out, *d_k_out;
+  uint32_t q_heads, k_heads;
+  float eps;
+  int32_t dtype;
+} ltc_rotate_rows;
+
+int ltc_norm_rotate(const ltc_rotation* rotation, const ltc_cache_seqs* seqs, const ltc_rotate_rows* rows,
+                    hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -124,7 +124,7 @@ def lib():
         L.ltc_cache_evict_workspace_size.argtypes = [vp, vp]
         L.ltc_cache_evict_workspace_size.restype = u64
         L.ltc_cache_evict.argtypes = [vp, vp, vp, vp, u64, u32, u32, u32, vp, vp, vp, u64, vp]
-        L.ltc_norm_rotate.argtypes = [vp, vp, i32, vp, u32, vp, vp, u32, vp, ctypes.c_float, vp, vp, vp]
+        L.ltc_norm_rotate.argtypes = [vp, vp, vp, vp]
         for name in ("ltc_cache_write", "ltc_cache_read", "ltc_cache_attend",
                      "ltc_cache_attend_weigh", "ltc_cache_evict", "ltc_norm_rotate",
                      "ltc_compress_workspace_size", "ltc_compress_batch_workspace_size",

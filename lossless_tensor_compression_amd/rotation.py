@@ -13,6 +13,7 @@ backward pass: tensors that require a gradient are refused.
 """
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -20,6 +21,7 @@ from . import LTCError, _check, lib
 from . import kv_cache as _kc
 
 _INT32 = torch.int32
+_pack_rest = struct.Struct("=QQQQIIfi").pack  # ltc_rotate_rows behind its two ltc_cache_rows
 
 
 class RotationStruct(ctypes.Structure):
@@ -63,7 +65,7 @@ class Rotation:
         self.turns = torch.tensor(turns, dtype=torch.int64, device=device)
         self.device = self.turns.device
         self.status = torch.zeros(1, dtype=_INT32, device=device)
-        self._index = self.turns.get_device()
+        self._index, self._shape = self.turns.get_device(), torch.Size((dim,))
         self._lib = lib()
         self._struct = RotationStruct(self.turns.data_ptr(), self.status.data_ptr(), dim, rotary, int(self.pairs), 0)
         self._ref = ctypes.byref(self._struct)
@@ -77,31 +79,13 @@ class Rotation:
             raise LTCError(-5, "lengths or cu that contradict each other")
 
 
-def _seqs(gpu, lengths, cu, rows):
-    if not (lengths.dtype is _INT32 and lengths.get_device() == gpu
-            and (cu is None or cu.dtype is _INT32 and cu.get_device() == gpu)):
-        raise ValueError("lengths and cu must be int32 on the rotation's GPU")
-    seqs = lengths.numel()
-    if lengths.dim() != 1 or not lengths.is_contiguous():
-        raise ValueError("lengths must be contiguous [sequences]")
-    if cu is None:
-        if rows != seqs:
-            raise ValueError("without cu there is one row for each sequence")
-    elif cu.dim() != 1 or cu.numel() != seqs + 1 or not cu.is_contiguous():
-        raise ValueError("cu must be contiguous [sequences + 1]")
-    return _kc._pack_seqs(0, lengths.data_ptr(), 0 if cu is None else cu.data_ptr(), 0, seqs, rows, 0, 0)
-
-
 def _weight(t, rotation, dtype, name):
-    if t is None:
-        return None, None
-    if t.dtype is not dtype or t.get_device() != rotation._index or t.shape != (rotation.dim,):
+    """t in a form that the kernel takes (a copy where it is not)."""
+    if t.dtype is not dtype or t.get_device() != rotation._index or t.shape != rotation._shape:
         raise ValueError(f"{name} must be {dtype} [{rotation.dim}] on the rotation's GPU")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient, which norm_rotate has not: call under torch.no_grad()")
-    if t.stride(0) != 1 or t.data_ptr() % 16:
-        t = t.clone(memory_format=torch.contiguous_format)
-    return t, t.data_ptr()
+    return t if t.stride(0) == 1 and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
 def norm_rotate(q, k, rotation, lengths, cu=None, q_weight=None, k_weight=None, eps=1e-6):
@@ -113,6 +97,7 @@ def norm_rotate(q, k, rotation, lengths, cu=None, q_weight=None, k_weight=None, 
     if _kc._current_gpu() != gpu:
         with torch.cuda.device(gpu):
             return norm_rotate(q, k, rotation, lengths, cu, q_weight, k_weight, eps)
+    # straight code from here: it is most of a small call's time
     dtype = q.dtype
     if dtype not in _kc.CACHE_DTYPES:
         raise LTCError(-2, f"dtype {dtype}")
@@ -120,13 +105,27 @@ def norm_rotate(q, k, rotation, lengths, cu=None, q_weight=None, k_weight=None, 
         raise ValueError("q and k must be of one type, on the rotation's GPU")
     q, qr, q_shape = _kc._take_rows(q, None, rotation.dim, "q")
     k, kr, k_shape = _kc._take_rows(k, None, rotation.dim, "k")
-    if q_shape[0] != k_shape[0]:
+    rows = q_shape[0]
+    if rows != k_shape[0]:
         raise ValueError("one key row for each query row")
-    s = _seqs(gpu, lengths, cu, q_shape[0])
-    q_weight, qw = _weight(q_weight, rotation, dtype, "q_weight")
-    k_weight, kw = _weight(k_weight, rotation, dtype, "k_weight")
-    q_out = torch.empty(q_shape, dtype=dtype, device=rotation.device)
-    k_out = torch.empty(k_shape, dtype=dtype, device=rotation.device)
-    _check(rotation._lib.ltc_norm_rotate(rotation._ref, s, _kc.CACHE_DTYPES[dtype], qr, q_shape[1], qw, kr, k_shape[1], kw, eps,
-                                         q_out.data_ptr(), k_out.data_ptr(), _kc._raw_stream(gpu)), "norm_rotate")
+    if not (lengths.dtype is _INT32 and lengths.get_device() == gpu
+            and (cu is None or cu.dtype is _INT32 and cu.get_device() == gpu)):
+        raise ValueError("lengths and cu must be int32 on the rotation's GPU")
+    seqs = lengths.numel()
+    if lengths.dim() != 1 or not lengths.is_contiguous():
+        raise ValueError("lengths must be contiguous [sequences]")
+    if cu is None:
+        if rows != seqs:
+            raise ValueError("without cu there is one row for each sequence")
+    elif cu.dim() != 1 or cu.numel() != seqs + 1 or not cu.is_contiguous():
+        raise ValueError("cu must be contiguous [sequences + 1]")
+    if q_weight is not None:
+        q_weight = _weight(q_weight, rotation, dtype, "q_weight")
+    if k_weight is not None:
+        k_weight = _weight(k_weight, rotation, dtype, "k_weight")
+    q_out, k_out = q.new_empty(q_shape), k.new_empty(k_shape)
+    s = _kc._pack_seqs(0, lengths.data_ptr(), 0 if cu is None else cu.data_ptr(), 0, seqs, rows, 0, 0)
+    r = qr + kr + _pack_rest(0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
+                             q_out.data_ptr(), k_out.data_ptr(), q_shape[1], k_shape[1], eps, _kc.CACHE_DTYPES[dtype])
+    _check(rotation._lib.ltc_norm_rotate(rotation._ref, s, r, _kc._raw_stream(gpu)), "norm_rotate")
     return q_out, k_out
