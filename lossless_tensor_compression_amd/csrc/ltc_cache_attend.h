@@ -227,6 +227,7 @@ __device__ __forceinline__ float rebase(float l, float from, float to) {
 // What a wave keeps of its 16 * NC rows; lane 16 g + n has row n of each 16.
 // Eight: eight numbers as the first product takes them, fp16; bf16 from a bf16
 // cache of 4-bit codes.
+struct NoQueries {};  // they are held elsewhere (Queries8)
 template <int D, int NC, class Eight = half8> struct Rows {
   Eight q[NC][D / 32];     // the k-group g of the queries, times 2^up
   int up[NC];              // 0 from a cache of 4-bit codes
@@ -241,6 +242,7 @@ template <int CODES, int D, int NC, class Eight>
 __device__ __forceinline__ void load_rows(Rows<D, NC, Eight>& w, const AttendArgs& a, const Span& sp, uint32_t head, uint32_t G,
                                           uint32_t r0, uint32_t packed, bool bf16, int n, int g) {
   constexpr int KS = D / 32;
+  constexpr bool kLoad = !std::is_same<Eight, NoQueries>::value;
   for (int nc = 0; nc < NC; ++nc) {
     const uint32_t r = r0 + nc * 16 + n;
     const bool live = r < packed;
@@ -249,11 +251,12 @@ __device__ __forceinline__ void load_rows(Rows<D, NC, Eight>& w, const AttendArg
     w.hi[nc] = live ? (int)(sp.start + token) + 1 : 0;
     w.lo[nc] = a.window ? max(w.hi[nc] - (int)a.window, 0) : 0;
     uint4v raw[KS];
-    for (int x = 0; x < KS; ++x) {
+    for (int x = 0; x < KS && kLoad; ++x) {
       raw[x] = live ? *reinterpret_cast<const uint4v*>(src + dim_of<CODES, D>(x, g)) : uint4v{0, 0, 0, 0};
     }
     w.up[nc] = 0;
-    if constexpr (CODES == LTC_E2M1) {
+    if constexpr (!kLoad) {
+    } else if constexpr (CODES == LTC_E2M1) {
       for (int x = 0; x < KS; ++x) w.q[nc][x] = __builtin_bit_cast(Eight, raw[x]);
     } else if (bf16) {
       // to fp16 by a power of two that brings the row's largest number to
@@ -279,6 +282,53 @@ __device__ __forceinline__ void load_rows(Rows<D, NC, Eight>& w, const AttendArg
     w.l[nc] = 0.0f;
     w.nan[nc] = 0;
     for (int i = 0; i < D / 16; ++i) w.acc[nc][i] = float4v{0, 0, 0, 0};
+  }
+}
+
+// bf16 queries against keys of 4 bits, 128 dims a product: the matrix cores take
+// the codes as they are, with a scale for each token and 32 dims, if the other
+// operand is 8 bits.  So a query goes in as two E4M3 numbers, q 2^s = high + low /
+// 16 with the row's largest in 2^7..2^8.  high keeps 4 of bf16's 8 bits, rounded,
+// which leaves 4 for low: exact, but for numbers below 2^-13 of the row's largest,
+// which keep 2^-21 of it.  A lane's 32 numbers are dims 16 g .. + 15 and 64 on.
+typedef int int8v __attribute__((ext_vector_type(8)));
+template <int D, int NC> struct Queries8 {
+  int8v part[2][NC][D / 128];  // high, low
+  int scale[2][NC];            // bytes of their exponents
+};
+
+template <int D, int NC>
+__device__ __forceinline__ void load_queries8(Queries8<D, NC>& q, const AttendArgs& a, const Span& sp, uint32_t head,
+                                              uint32_t G, uint32_t r0, uint32_t packed, int n, int g) {
+  for (int nc = 0; nc < NC; ++nc) {
+    const uint32_t r = r0 + nc * 16 + n;
+    const bool live = r < packed;
+    const uint32_t token = live ? r / G : 0, qh = head * G + (live ? r % G : 0);
+    const uint16_t* src = a.q.base + (uint64_t)(sp.row0 + token) * a.q.row_stride + (uint64_t)qh * a.q.head_stride;
+    uint4v raw[D / 128][4];
+    uint32_t top = 0;
+    for (int j = 0; j < D / 128; ++j)
+      for (int i = 0; i < 4; ++i) {
+        raw[j][i] = live ? *reinterpret_cast<const uint4v*>(src + j * 128 + i / 2 * 64 + g * 16 + i % 2 * 8) : uint4v{0, 0, 0, 0};
+        for (int w = 0; w < 4; ++w) top = max(top, max(raw[j][i][w] & 0x7fffu, (raw[j][i][w] >> 16) & 0x7fffu));
+      }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    const int up = min(134 - (int)(top >> 7), 122);  // the low part's exponent is a byte, too
+    q.scale[0][nc] = 127 - up;
+    q.scale[1][nc] = 123 - up;
+    const float f = power_of_two(up);
+    for (int j = 0; j < D / 128; ++j)
+      for (int w = 0; w < 8; ++w) {
+        const uint32_t x = raw[j][w / 2][w % 2 * 2], y = raw[j][w / 2][w % 2 * 2 + 1];
+        const float4v v = float4v{widen<LTC_BF16>(x & 0xffffu), widen<LTC_BF16>(x >> 16), widen<LTC_BF16>(y & 0xffffu),
+                                  widen<LTC_BF16>(y >> 16)} * f;
+        const uint32_t high = to_codes<true>(v);
+        q.part[0][nc][j][w] = (int)high;
+        q.part[1][nc][j][w] = (int)to_codes<true>((v - code_values<true>(high)) * 16.0f);
+        // infinities and NaN make the row NaN
+        if (top >= 0x7f80u) q.part[0][nc][j][w] = q.part[1][nc][j][w] = 0x7f7f7f7f;
+      }
   }
 }
 
@@ -348,19 +398,30 @@ __device__ __forceinline__ float key_factor(uint32_t byte, float f) { return f *
 __device__ __forceinline__ float value_exponent(uint32_t byte) { return (float)((int)byte - 127); }
 __device__ __forceinline__ float value_inverse(uint32_t byte) { return power_of_two(127 - kHead - (int)byte); }
 
+// What the products are multiplied with: a factor for each token, or one for all
+// where the matrix cores have seen to the keys' scales.
+struct FactorOfTokens {
+  const Tokens4& of;
+  __device__ __forceinline__ float4v operator()(int t) const { return *reinterpret_cast<const float4v*>(&of.f[0][t]); }
+};
+struct OneFactor {
+  float f;
+  __device__ __forceinline__ float4v operator()(int) const { return float4v{f, f, f, f}; }
+};
+
 // far: some token's w lies more than kSpread from a first one's, here or in a step
 // before.  Else every weight that counts below the fraction is one above it too.
 constexpr int kSpread = 30;
 
 // The products of a step to weights.
-template <int D, int NC, class Eight>
-__device__ __forceinline__ void step_weights4(Rows<D, NC, Eight>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], const Tokens4& of,
-                                              int tv, bool edge, bool have, bool far) {
+template <int D, int NC, class Eight, class Factor>
+__device__ __forceinline__ void step_weights4(Rows<D, NC, Eight>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], const Factor& factor_of,
+                                              const Tokens4& of, int tv, bool edge, bool have, bool far) {
   const int own = tv & (kStep - 1);
   float4v factor[4], wv[4];
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
-    factor[b] = *reinterpret_cast<const float4v*>(&of.f[0][own + 4 * b]);
+    factor[b] = factor_of(own + 4 * b);
     wv[b] = *reinterpret_cast<const float4v*>(&of.f[1][own + 4 * b]);
   }
 #pragma unroll
@@ -678,7 +739,7 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC, CODES == LTC_E2M1)) v
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      step_weights4(w, st, p, lds_tokens[wave], tv, edge, have_v, far);
+      step_weights4(w, st, p, FactorOfTokens{lds_tokens[wave]}, lds_tokens[wave], tv, edge, have_v, far);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
     } else {
@@ -922,11 +983,14 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
   constexpr bool kFour = CODES == LTC_E2M1;
   constexpr uint32_t kBlockBytes = kFour ? 8 * D : 16 * D;
   constexpr int VB = kFour ? DB / 2 : DB, VL = (VB + 3) / 4;
-  typedef typename std::conditional<kFour && BF, bf8, half8>::type Eight;
-  __shared__ half8 lds[2][(KS * 4 + DB * 2) * 64];  // keys [x][b][lane], values [i][h][lane]
+  constexpr bool kScaled = kFour && BF && D % 128 == 0;  // Queries8
+  typedef typename std::conditional<kScaled, NoQueries, typename std::conditional<kFour && BF, bf8, half8>::type>::type Eight;
+  constexpr int KX = kScaled ? D / 128 : KS;        // the first product's instructions for a block
+  __shared__ half8 lds[2][(KX * 4 + DB * 2) * 64];  // keys [x][b][lane], values [i][h][lane]
   __shared__ Tokens4 lds_tokens[kFour ? 2 : 1];
+  __shared__ uint32_t lds_scales[2][kScaled ? KX : 1][64];  // byte b: the exponent of the lane's 32 dims in block b
   __shared__ int lds_nan[2];                        // 1 + the step whose values have a NaN
-  constexpr int kValues = KS * 4;
+  constexpr int kValues = KX * 4;
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t head, unit, split;
@@ -957,6 +1021,8 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
   const int lo = a.window ? max(all_hi - (int)a.window, 0) : 0, all_lo = a.window ? max(hi - (int)a.window, 0) : 0;
   Rows<D, NC, Eight> w;
   load_rows<CODES, D, NC>(w, a, sp, head, G, w0, packed, bf16, n, g);
+  Queries8<kScaled ? D : 128, NC> q8;
+  if constexpr (kScaled) load_queries8<D, NC>(q8, a, sp, head, G, w0, packed, n, g);
 
   const uint32_t page_mask = (1u << c.page_log) - 1;
   const int kb = n >> 2;
@@ -972,6 +1038,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
   uint2v kt = {0, 0};
   Keys4<D> kq;
   uint32_t exps[2] = {};  // the bytes of a token's exponents, key and value, of the step to turn next
+  uint32_t key_exp = 0;   // and that of the token whose keys the lane reads
   int first_w = -1;       // the first one's
   bool far = false;
   int32_t k_page = -1, v_page = -1;           // of the step to load next
@@ -989,7 +1056,8 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
       const uint8_t* sk = c.scales + token_scales(c, (uint32_t)k_page < c.pages ? (uint32_t)k_page : 0, head);
       const uint8_t* sv = c.scales + token_scales(c, (uint32_t)v_page < c.pages ? (uint32_t)v_page : 0, head);
       kq.load(k, sk + 2 * (page_mask + 1) + (((uint32_t)tk & page_mask) + (n & 3) + 4 * wave) * drop_bytes(D), g);
-      exps[0] = sv[((uint32_t)tv & page_mask) + n];
+      if constexpr (kScaled) key_exp = sk[((uint32_t)tk & page_mask) + (n & 3) + 4 * wave];
+      else exps[0] = sv[((uint32_t)tv & page_mask) + n];
       exps[1] = sv[((uint32_t)tv & page_mask) + n + page_mask + 1];
     } else {
       for (int j = 0; j < KL; ++j) kr[j] = *reinterpret_cast<const uint4v*>(k + g * 256 + j * 1024);
@@ -1006,14 +1074,22 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
   auto turn = [&](int step) {
     half8* to = lds[step & 1] + lane;
     if constexpr (kFour) {
-      for (int x = 0; x < KS; ++x)
-        to[(x * 4 + wave) * 64] =
-            __builtin_bit_cast(half8, codes_as<CODES, BF ? LTC_BF16 : LTC_FP16>(kq.c[x], 0, kq.scale(x, g)));
+      if constexpr (kScaled) {
+        for (int x = 0; x < KX; ++x) {
+          to[(x * 4 + wave) * 64] = __builtin_bit_cast(half8, uint4v{kq.c[4 * x], kq.c[4 * x + 1], kq.c[4 * x + 2], kq.c[4 * x + 3]});
+          const int e = (int)key_exp - (int)(kq.drops >> (4 * (4 * x + g)) & 15);
+          reinterpret_cast<uint8_t*>(&lds_scales[step & 1][x][lane])[wave] = (uint8_t)max(e, 0);
+        }
+      } else {
+        for (int x = 0; x < KS; ++x)
+          to[(x * 4 + wave) * 64] =
+              __builtin_bit_cast(half8, codes_as<CODES, BF ? LTC_BF16 : LTC_FP16>(kq.c[x], 0, kq.scale(x, g)));
+      }
       for (int i = 0; i < VL; ++i)
         if (VB % 4 == 0 || wave + 4 * i < VB)
           for (int h = 0; h < 4; ++h) to[(kValues + 4 * (wave + 4 * i) + h) * 64] = codes4_to_half(vr[i][h], 1.0f);
       Tokens4& of = lds_tokens[step & 1];
-      if (wave == 0) of.f[0][lane] = key_factor(exps[0], base * power_of_two(-kLift));
+      if (wave == 0 && !kScaled) of.f[0][lane] = key_factor(exps[0], base * power_of_two(-kLift));
       if (wave == 1) of.f[1][lane] = value_exponent(exps[1]);
       if (wave == 2) of.f[2][lane] = value_inverse(exps[1]);
       if (first_w < 0) first_w = __builtin_amdgcn_readfirstlane((int)exps[1]);
@@ -1079,21 +1155,47 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
     float4v st[NC][4];
     for (int nc = 0; nc < NC; ++nc)
       for (int b = 0; b < 4; ++b) st[nc][b] = float4v{0, 0, 0, 0};
+    if constexpr (kScaled) {
 #pragma unroll
-    for (int x = 0; x < KS; ++x)
+      for (int x = 0; x < KX; ++x) {
+        const int exponents = (int)lds_scales[step & 1][x][lane];
+        int8v k[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const Eight k8 = __builtin_bit_cast(Eight, from[(x * 4 + b) * 64]);
+        for (int b = 0; b < 4; ++b) {
+          const uint4v y = __builtin_bit_cast(uint4v, from[(x * 4 + b) * 64]);
+          k[b] = int8v{(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0};
+        }
 #pragma unroll
-        for (int nc = 0; nc < NC; ++nc) st[nc][b] = product(k8, w.q[nc][x], st[nc][b]);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) {
+            const int8v q = q8.part[h][nc][x];
+            const int e = q8.scale[h][nc];
+            // 4: E2M1, 0: E4M3; then which byte of the exponents
+            st[nc][0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k[0], q, st[nc][0], 4, 0, 0, exponents, 0, e);
+            st[nc][1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k[1], q, st[nc][1], 4, 0, 1, exponents, 0, e);
+            st[nc][2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k[2], q, st[nc][2], 4, 0, 2, exponents, 0, e);
+            st[nc][3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k[3], q, st[nc][3], 4, 0, 3, exponents, 0, e);
+          }
       }
-    reads_ahead<KS, NC>();
+    } else {
+#pragma unroll
+      for (int x = 0; x < KS; ++x)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const Eight k8 = __builtin_bit_cast(Eight, from[(x * 4 + b) * 64]);
+#pragma unroll
+          for (int nc = 0; nc < NC; ++nc) st[nc][b] = product(k8, w.q[nc][x], st[nc][b]);
+        }
+      reads_ahead<KS, NC>();
+    }
     // ---- weights
     const bool lost = tv < hi && tv + 16 > lo && !have;
     if (lost && n == 0) report(c, kCacheBadPage);
     const bool edge = t0 < all_lo || t0 + kStep > all_hi || __any(lost);
     half8 p[NC][2];
-    if constexpr (kFour) step_weights4(w, st, p, lds_tokens[step & 1], tv, edge, have, far);
+    if constexpr (kScaled) step_weights4(w, st, p, OneFactor{fmaxf(base, 0x1p-126f)}, lds_tokens[step & 1], tv, edge, have, far);
+    else if constexpr (kFour) step_weights4(w, st, p, FactorOfTokens{lds_tokens[step & 1]}, lds_tokens[step & 1], tv, edge, have, far);
     else step_weights<D, NC>(w, st, p, base, sc, tv, edge, have);
     // ---- O^T
     from += kValues * 64;
