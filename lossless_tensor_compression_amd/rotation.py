@@ -21,6 +21,7 @@ from . import LTCError, _check, lib
 from . import kv_cache as _kc
 
 _INT32 = torch.int32
+_empty_like, _contiguous = torch.empty_like, torch.contiguous_format
 _pack_rest = struct.Struct("=QQQQIIfi").pack  # ltc_rotate_rows behind its two ltc_cache_rows
 
 
@@ -123,7 +124,8 @@ def norm_rotate(q, k, rotation, lengths, cu=None, q_weight=None, k_weight=None, 
         q_weight = _weight(q_weight, rotation, dtype, "q_weight")
     if k_weight is not None:
         k_weight = _weight(k_weight, rotation, dtype, "k_weight")
-    q_out, k_out = q.new_empty(q_shape), k.new_empty(k_shape)
+    # half the time of torch.empty with a shape
+    q_out, k_out = _empty_like(q, memory_format=_contiguous), _empty_like(k, memory_format=_contiguous)
     s = _kc._pack_seqs(0, lengths.data_ptr(), 0 if cu is None else cu.data_ptr(), 0, seqs, rows, 0, 0)
     r = qr + kr + _pack_rest(0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
                              q_out.data_ptr(), k_out.data_ptr(), q_shape[1], k_shape[1], eps, _kc.CACHE_DTYPES[dtype])

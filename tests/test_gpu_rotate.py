@@ -121,6 +121,12 @@ def test_many_sequences(ltc):
     check(ltc, FP, 96, 2, 1, [2, 0, 3], [5, 6, 7], front=3, behind=4)
 
 
+@pytest.mark.parametrize("dim", [64, 96, 192])
+def test_many_rows(ltc, dim):
+    """More than the rows that four waves share."""
+    check(ltc, BF, dim, 5, 2, [700, 1, 0, 400], [5, 60000, 3, 0], pairs=dim == 96)
+
+
 def test_strided_parts_of_one_tensor(ltc):
     qkv = torch.randn(10, 12, 128, device="cuda").to(BF)
     rot = ltc.Rotation(128)
