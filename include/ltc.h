@@ -448,12 +448,13 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
                               int32_t* d_status, hipStream_t stream, const hipEvent_t* h_events);
 
 /* ---------------------------------------------------------------------------
- * THE 8-BIT KEY/VALUE CACHE.  Keys and values of a served model, quantised as
- * they are written, read back, and attended to in place.
+ * THE KEY/VALUE CACHE, in 8 or 4 bits.  Keys and values of a served model,
+ * quantised as they are written, read back, attended to in place, and cut to
+ * the positions that were worth most.
  *
  * The cache is `pages` pages of `page` tokens (16, 32, 64, 128 or 256), each
- * for `heads` heads of `dim` numbers (64, 96, 128, 192 or 256), with one
- * power-of-two scale for each page, head and kind (key, value):
+ * for `heads` heads of `dim` numbers (64, 96, 128, 192 or 256).  In 8 bits, with
+ * one power-of-two scale for each page, head and kind (key, value):
  *   k_codes u8 [pages][heads][page/16][dim/16][16 tokens][16 dims]
  *   v_codes u8 [pages][heads][page/16][dim][16 tokens]
  *   scales  u8 [pages][heads][2] (key, value); a scale is 2^(byte - 127), byte
@@ -461,6 +462,16 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
  * Codes are OCP E4M3 (LTC_E4M3) or two's-complement integers (LTC_INT8); a
  * number is its code times its scale.  The layouts are those in which the
  * matrix cores take 16 tokens of keys and values.
+ * In 4 bits (LTC_E2M1), with a scale for each token, head and kind:
+ *   k_codes u8 [pages][heads][page/16][dim/32][16 tokens][16], two dims a byte
+ *   v_codes u8 [pages][heads][page/16][dim][8], two tokens a byte
+ *   scales  u8 [pages][heads][page * (2 + drops)]: page bytes of keys' exponents,
+ *           page bytes of values', and `drops` bytes for each token (1, 2, 2, 4,
+ *           4 for the five dims), nibble j for dims 32 j .. 32 j + 31 of its key;
+ *           what is left of them is 0
+ * the first of two in the low half.  Codes are OCP E2M1: 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6 and, from 8 on, their negatives.  A value is its code times 2^(byte - 127), a
+ * key its code times 2^(byte - 127 - nibble).  Bytes are 27..253 (2^-100 to 2^126).
  *
  * A call's rows belong to sequences: rows cu[i]..cu[i+1] to sequence i, as its
  * last positions, lengths[i] - (cu[i+1] - cu[i]) to lengths[i] - 1.  Position t
@@ -483,16 +494,16 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
  * Argument errors that the host sees (types, sizes, null or misaligned
  * pointers, more than 2^24 rows or 2^20 sequences) return before anything is
  * enqueued.  A call without rows or sequences succeeds and does nothing. */
-enum { LTC_E4M3 = 0, LTC_INT8 = 1, LTC_E2M1 = 3 };
+enum { LTC_E4M3 = 0, LTC_INT8 = 1, LTC_E2M1 = 3 };  /* 2 is no code type */
 enum { LTC_CACHE_BAD_PAGE = 1, LTC_CACHE_BAD_SEQUENCE = 2 };
 
 typedef struct {
   void* d_k_codes;     /* 16-byte aligned, like d_v_codes */
   void* d_v_codes;
-  void* d_scales;      /* 2-byte aligned */
+  void* d_scales;      /* 2-byte aligned; of LTC_E2M1 16-byte */
   uint32_t* d_status;  /* one word */
   uint32_t pages, heads, dim, page;
-  int32_t codes;       /* LTC_E4M3 or LTC_INT8 */
+  int32_t codes;       /* LTC_E4M3, LTC_INT8 or LTC_E2M1 */
   int32_t dtype;       /* LTC_BF16 or LTC_FP16: keys, values, queries and outputs of the calls */
 } ltc_cache;
 
@@ -513,15 +524,19 @@ typedef struct {
   uint64_t row_stride, head_stride;
 } ltc_cache_rows;
 
-/* Write keys and values [rows][heads][dim] to their positions.  The scale of a
+/* Write keys and values [rows][heads][dim] to their positions.  In 8 bits: the scale of a
  * page and head is the smallest power of two, not below 2^-100, for which the
  * largest magnitude among the page's new rows fits the codes (448 in E4M3, 127
  * in INT8); a page that holds earlier positions of the sequence keeps its scale
  * if that is larger, and if it is smaller the earlier tokens' codes are divided
  * by the growth and rounded again.  Numbers are rounded to the nearest code,
  * ties to even.  Infinities do not count for the scale and saturate; a NaN
- * becomes E4M3's NaN, or 0 in INT8.  Tokens behind a sequence's end are left as
- * they are.  No two sequences of a call may write to the same page. */
+ * becomes E4M3's NaN, or 0 in INT8.  In 4 bits a token's exponent is the least,
+ * not below -100, for which its head's largest magnitude fits the codes (6), and a
+ * nibble the most, up to 15, by which its 32 dims of a key could have a smaller
+ * one (15 for zeros); rounding, infinities and NaN as in INT8, and no other token's
+ * codes change.  Tokens behind a sequence's end are left as they are.  No two
+ * sequences of a call may write to the same page. */
 int ltc_cache_write(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* k,
                     const ltc_cache_rows* v, hipStream_t stream);
 
@@ -541,6 +556,10 @@ int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k
  * bits down to 2^-23 of the largest weight times its page's value scale
  * (below 2^-34 of it they are lost); scores and sums are held in fp32, and
  * |scale * q k| is to stay below 2^25 (past it weights lose all their bits).
+ * (With 4-bit codes read a weight's token for its page.  There, bf16 queries of
+ * 128 or 256 dims in calls of many rows enter the products as sums of two E4M3
+ * numbers: exactly, but for numbers below 2^-13 of their head's largest, which
+ * keep 2^-21 of it.)
  * A result depends on the call's shapes, not on timing.  The workspace has
  * ltc_cache_attend_workspace_size() bytes, 256-byte aligned (none may be
  * needed, then d_ws may be NULL).  Its first LTC_CACHE_WS_ZEROS bytes must
@@ -553,31 +572,76 @@ uint64_t ltc_cache_attend_workspace_size(const ltc_cache* cache, const ltc_cache
 int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
                      uint32_t window, float scale, void* d_out, void* d_ws, uint64_t ws_nbytes, hipStream_t stream);
 
+/* The same, and what each position was worth to the rows: d_weights, fp32
+ * [pages][heads][page], gets at a position's page and token, for each head, the sum
+ * of the softmax's weights of all rows that see it and all query heads that read
+ * the head, added to what it held; what the positions of the call's own rows held
+ * does not count, and positions that no row sees keep what they have.  No two
+ * sequences of a call may share a page.  A NaN in a row's output comes with NaN at
+ * the positions that the row sees (or, from a NaN among values, with none).
+ * Weights below 2^-126 count as 0.  Bad pages and sequences as above; their weights
+ * are left.  d_out is the same as ltc_cache_attend's.  The workspace is one for
+ * ltc_cache_attend as well, where it is large enough, and the other way round. */
 uint64_t ltc_cache_attend_weigh_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,
                                                uint32_t window);
 int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
                            uint32_t window, float scale, void* d_out, float* d_weights, void* d_ws, uint64_t ws_nbytes,
                            hipStream_t stream);
 
+/* Cut sequences to `keep` positions (1 at least): the last `recent` of them, and of
+ * the others the keep - recent of largest weight (d_weights as above, 16-byte
+ * aligned; of equal ones the first, a NaN below all numbers), each head by itself.
+ * They are moved, in their order and with their weights, to the pages d_to[i][0 ..],
+ * rows of it to_stride apart, to_width >= keep / page rounded up: position j of a
+ * head's kept ones is token j % page of page d_to[i][j / page].  A sequence of no
+ * more than `keep` positions is moved whole.  Of seqs the table, the lengths and the
+ * number of sequences count (65,535 at most; d_cu NULL, so rows = seqs), and keep is
+ * 65,535 pages at most.  d_lengths [seqs] gets the new lengths, d_positions
+ * [seqs][heads][keep] the kept positions, in order and -1 behind the last.
+ * Pages of d_to must not be in use: neither named by a table below its length, nor
+ * twice here.  What lies behind a sequence's new end in its last page is left.
+ * 4-bit codes are moved as they are.  An 8-bit page gets the largest scale that one
+ * of its tokens had, and codes of smaller scales are divided by the growth and
+ * rounded again.  A position without a page has a weight below all numbers; if it is
+ * kept, it becomes zeros (with the lowest exponents) of weight 0 and is reported, and
+ * so is a page of d_to outside the cache, which is not written.  A sequence whose
+ * length is negative or past its table is reported and gets length 0.
+ * The workspace, of which none may be needed, is like ltc_cache_attend's, whose zeros
+ * it leaves alone. */
 uint64_t ltc_cache_evict_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs);
 int ltc_cache_evict(const ltc_cache* cache, const ltc_cache_seqs* seqs, float* d_weights, const int32_t* d_to,
                     uint64_t to_stride, uint32_t to_width, uint32_t keep, uint32_t recent, int32_t* d_lengths,
                     int32_t* d_positions, void* d_ws, uint64_t ws_nbytes, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * QUERIES AND KEYS ON THEIR WAY TO THE CACHE: the norm of each head and the
+ * rotation by the row's position, in one pass.  x becomes
+ *   y = x / sqrt(mean(x^2) + eps) * weight    (without a weight: y = x)
+ * and then, of the first `rotary` dims (a multiple of 16, up to dim), pair i
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * of the angle position * rate_i; the pairs are dims i and i + rotary / 2, or, with
+ * pairs = 1, dims 2 i and 2 i + 1.  d_turns[i] is rate_i / 2 pi, modulo 1, in units of
+ * 2^-64, so an angle is exact to 2^-32 of a turn whatever the position (which is
+ * below 2^31).  Computed in fp32 and rounded once.
+ * Rows belong to sequences as in the cache's calls (of ltc_cache_seqs the table does
+ * not count); lengths count the positions a sequence has come to, which are more than
+ * its cache holds once that has been cut.  Rows of no sequence get zeros, and so do
+ * those of a refused one, which sets LTC_CACHE_BAD_SEQUENCE in *d_status. */
 typedef struct {
-  const uint64_t* d_turns;
-  uint32_t* d_status;
-  uint32_t dim, rotary, pairs;
-  uint32_t reserved;
+  const uint64_t* d_turns;  /* [rotary / 2], 8-byte aligned; may be NULL if rotary is 0 */
+  uint32_t* d_status;       /* one word */
+  uint32_t dim;             /* 64, 96, 128, 192 or 256 */
+  uint32_t rotary, pairs;
+  uint32_t reserved;        /* 0 */
 } ltc_rotation;
 
 typedef struct {
-  ltc_cache_rows q, k;
-  const void *d_q_weight, *d_k_weight;
-  void *d_q_out, *d_k_out;
-  uint32_t q_heads, k_heads;
+  ltc_cache_rows q, k;                  /* [rows][q_heads][dim] and [rows][k_heads][dim] */
+  const void *d_q_weight, *d_k_weight;  /* [dim] of dtype, 16-byte aligned, or NULL */
+  void *d_q_out, *d_k_out;              /* like q and k without strides, 16-byte aligned */
+  uint32_t q_heads, k_heads;            /* 65,535 at most; 0: that side is left out */
   float eps;
-  int32_t dtype;
+  int32_t dtype;                        /* LTC_BF16 or LTC_FP16 */
 } ltc_rotate_rows;
 
 int ltc_norm_rotate(const ltc_rotation* rotation, const ltc_cache_seqs* seqs, const ltc_rotate_rows* rows,

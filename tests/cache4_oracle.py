@@ -131,7 +131,8 @@ def read(c, table, lengths, cu, rows):
     return k, v, status
 
 
-def attend(gather, heads, dim, page, q, table, lengths, cu=None, window=0, scale=None, top=TOP, value_scales=None):
+def attend(gather, heads, dim, page, q, table, lengths, cu=None, window=0, scale=None, top=TOP, value_scales=None,
+           query_error=0.0):
     """(out, slack, shares, share_slack, status) of attention over positions
     that gather(i, length, which) gives.  shares: a list with, for each
     sequence, the weights [heads, length] its positions got, and how far a
@@ -144,7 +145,8 @@ def attend(gather, heads, dim, page, q, table, lengths, cu=None, window=0, scale
         and in the maximum), two more of 2^-24 of |s| and the value's exponent
         with it, and 2^-22 for exp2;
       sums over n positions in fp32: n 2^-24 of the sum of magnitudes, above
-        and below the fraction.
+        and below the fraction;
+      query_error of the row's largest number, of every number of a query.
     A share has the errors of s and of the sum below its fraction, its own
     sum's over the rows, and for each row and query head 2^-126: below that, fp32's
     smallest normal number, the result of exp2 is 0."""
@@ -182,7 +184,8 @@ def attend(gather, heads, dim, page, q, table, lengths, cu=None, window=0, scale
                     share = p / p.sum()
                     out[r0 + r, h] = share @ vv
                     mean = share @ np.abs(vv)
-                    exp_err = 2 * (dim + 8) * 2.0 ** -24 * big + 8 * 2.0 ** -24 * (np.abs(s).max() + 300) + 2.0 ** -22
+                    lost = scale * query_error * np.abs(qr).max() * np.abs(kk).sum(-1).max()
+                    exp_err = 2 * lost + 2 * (dim + 8) * 2.0 ** -24 * big + 8 * 2.0 ** -24 * (np.abs(s).max() + 300) + 2.0 ** -22
                     err = 2.0 ** -11 + exp_err + 2 * m * 2.0 ** -24
                     floor = m * 2.0 ** -25 * (share * vs[h // G, seen]).max() * top
                     slack[r0 + r, h] = 1.01 * (err * mean + floor)
@@ -192,7 +195,7 @@ def attend(gather, heads, dim, page, q, table, lengths, cu=None, window=0, scale
     return out, slack, shares, share_slack, status
 
 
-def attend4(c, q, table, lengths, cu=None, window=0, scale=None):
+def attend4(c, q, table, lengths, cu=None, window=0, scale=None, query_error=0.0):
     _, H, P, D = c["k"].shape
 
     def scales(i, length):
@@ -204,4 +207,4 @@ def attend4(c, q, table, lengths, cu=None, window=0, scale=None):
         return out[:, :length]
 
     return attend(lambda i, length, which: _gather(c, table, i, length, which), H, D, P, q, table, lengths, cu, window,
-                  scale, TOP, scales)
+                  scale, TOP, scales, query_error)

@@ -224,6 +224,76 @@ def test_small_drops_reach_the_scores(ltc):
         close(out, want, slack, BF)
 
 
+# calls of many rows: whose bf16 queries of 128 and 256 dims go in as two numbers of 8 bits
+MANY = {64: (8, 8, [300, 9] + [64] * 12), 128: (8, 8, [300, 9] + [64] * 12), 256: (8, 8, [150] + [64] * 10)}
+
+
+@pytest.mark.parametrize("small", [-3, -9, -13, -16, -20])
+@pytest.mark.parametrize("dim", [128, 256])
+def test_numbers_far_below_their_head_s_largest(ltc, dim, small):
+    """Queries with one large number, which meets keys of zero, and small ones that make the scores."""
+    heads, group, new = MANY[dim]
+    s = Setup4(ltc, 37, heads, dim, 32, BF, new, [5] * len(new))
+    s.o["k"][..., 7] = 0
+    s.upload(ltc)
+    q, _ = s.rows16(heads * group, 2.0 ** small)
+    q[..., 7] = 1.5
+    # scores of ordinary size
+    scale = dim ** -0.5 * 2.0 ** -small
+    out = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu, scale=scale)
+    want, slack, _, _, status = c4.attend4(s.o, q.double().cpu().numpy(), s.table, s.lengths, s.cu, 0, scale, 2.0 ** -21)
+    close(out, want, slack, BF)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_odd_queries_of_many_rows_stay_in_their_rows(ltc, dim, bad):
+    heads, group, new = MANY[dim]
+    s = Setup4(ltc, 38, heads, dim, 32, BF, new, [5] * len(new))
+    q, _ = s.rows16(heads * group, 1.0)
+    plain = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu)
+    q[3, 5, 9] = q[70, 0, dim - 1] = bad
+    out = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu)
+    nan = torch.isnan(out)
+    for r, h in ((3, 5), (70, 0)):
+        assert nan[r, h].all()
+        out[r, h] = plain[r, h]
+    assert torch.equal(out, plain) and int(nan.sum()) == 2 * dim
+
+
+@pytest.mark.parametrize("size", [2.0 ** -130, 2.0 ** -110, 2.0 ** -60, 2.0 ** 60, 2.0 ** 100])
+def test_queries_of_any_size_of_many_rows(ltc, size):
+    """Their power of two goes into the products, as far as fp32 has it."""
+    heads, group, new = MANY[128]
+    s = Setup4(ltc, 39, heads, 128, 32, BF, new, [5] * len(new))
+    e = round(np.log2(size))
+    for i, n in enumerate(s.lengths):
+        for j in range(-(-n // 32)):
+            s.o["ke"][s.table[i, j]] = (s.o["ke"][s.table[i, j]].astype(int) - e).clip(30, 250)
+    s.upload(ltc)
+    q, q64 = s.rows16(heads * group, size)
+    out = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu)
+    # queries of 2^-130 are subnormal: their 8 bits are fewer, and exact all the same
+    want, slack, _, _, _ = c4.attend4(s.o, q64, s.table, s.lengths, s.cu, query_error=2.0 ** -21 if size > 2.0 ** -115 else 2.0 ** -8)
+    close(out, want, slack, BF)
+
+
+@pytest.mark.parametrize("new,past,heads,group", [([1, 1, 1], [70, 80, 5], 1, 4), ([5, 9], [30, 40], 2, 4)])
+def test_infinite_queries_of_few_rows(ltc, new, past, heads, group):
+    """One row's infinity makes it NaN, whatever the signs of what it meets."""
+    for sign in (1, -1):
+        s = Setup4(ltc, 40, heads, 64, 32, BF, new, past)
+        s.o["k"][..., 7] = 3  # all positive: scores of one infinity
+        s.upload(ltc)
+        q, _ = s.rows16(heads * group, 1.0)
+        plain = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu)
+        q[1, 1, 7] = sign * float("inf")
+        out = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu)
+        assert torch.isnan(out[1, 1]).all()
+        out[1, 1] = plain[1, 1]
+        assert torch.equal(out, plain)
+
+
 def test_query_nan_stays_in_its_row(ltc):
     for new, past in (([1, 1, 1], [70, 80, 5]), ([150], [10])):
         s = Setup4(ltc, 34, 1, 64, 32, FP, new, past)
