@@ -16,7 +16,7 @@ OUT = os.path.join(HERE, "libltc.so")
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["ltc_compress.hip", "ltc_decompress.hip", "ltc_crc32.hip", "ltc_api.hip",
            "ltc_cache_store.hip", "ltc_cache_store4.hip", "ltc_cache_attend.hip", "ltc_cache_attend_int8.hip",
-           "ltc_cache_attend_e2m1.hip", "ltc_cache_weigh_e4m3.hip", "ltc_cache_weigh_int8.hip",
+           "ltc_cache_attend_e2m1.hip", "ltc_cache_weigh.hip", "ltc_cache_weigh_e4m3.hip", "ltc_cache_weigh_int8.hip",
            "ltc_cache_weigh_e2m1.hip", "ltc_cache_evict.hip", "ltc_rotate.hip", "ltc_cache_api.hip"]
 # plain C++ (no device code): the host-side parsing of blob bytes
 HOST_SOURCES = ["ltc_host.cpp"]

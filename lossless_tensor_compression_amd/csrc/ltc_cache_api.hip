@@ -89,7 +89,8 @@ int check_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_c
   a->window = window;
   a->scale = scale;
   a->ws = nullptr;
-  a->lse = nullptr;
+  a->lse = a->scores = nullptr;
+  a->scores_stride = 0;
   return LTC_OK;
 }
 
@@ -98,6 +99,11 @@ int check_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_c
 uint64_t lse_offset(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window) {
   const uint64_t need = cache_attend_workspace(c, s, codes, q_heads, window);
   return need < LTC_CACHE_WS_ZEROS ? (uint64_t)LTC_CACHE_WS_ZEROS : (need + 255) / 256 * 256;
+}
+
+// the scores lie behind them
+uint64_t scores_offset(const SeqView& s, uint32_t q_heads, uint64_t lse) {
+  return (lse + (uint64_t)s.rows * q_heads * sizeof(float) + 255) / 256 * 256;
 }
 
 int launched(hipError_t e) { return e == hipSuccess ? LTC_OK : LTC_ERR_HIP; }
@@ -162,7 +168,9 @@ uint64_t ltc_cache_attend_weigh_workspace_size(const ltc_cache* cache, const ltc
   CacheView c;
   SeqView s;
   if (check_cache(cache, &c) || check_seqs(seqs, &s) || check_heads(c, s, q_heads) || !s.rows) return 0;
-  return lse_offset(c, s, cache->codes, q_heads, window) + (uint64_t)s.rows * q_heads * sizeof(float);
+  const uint64_t stride = cache_scores_stride(c, s, cache->codes, q_heads, window);
+  return scores_offset(s, q_heads, lse_offset(c, s, cache->codes, q_heads, window)) +
+         stride * s.rows * q_heads * sizeof(float);
 }
 
 int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
@@ -173,13 +181,16 @@ int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, c
   AttendArgs a;
   const int rc = check_attend(cache, seqs, q, q_heads, window, scale, d_out, &c, &s, &a);
   if (rc || !s.rows) return rc;
-  if (c.pages && !aligned(d_weights, 4)) return LTC_ERR_INVALID_ARGUMENT;
-  const uint64_t lse = lse_offset(c, s, cache->codes, q_heads, window);
-  if (ws_nbytes < lse + (uint64_t)s.rows * q_heads * sizeof(float) || !aligned(d_ws, 256)) return LTC_ERR_WORKSPACE;
+  if (c.pages && !aligned(d_weights, 16)) return LTC_ERR_INVALID_ARGUMENT;
+  const uint64_t lse = lse_offset(c, s, cache->codes, q_heads, window), scores = scores_offset(s, q_heads, lse);
+  a.scores_stride = cache_scores_stride(c, s, cache->codes, q_heads, window);
+  if (ws_nbytes < scores + a.scores_stride * s.rows * q_heads * sizeof(float) || !aligned(d_ws, 256)) return LTC_ERR_WORKSPACE;
   a.ws = d_ws;
   a.lse = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + lse);
+  if (a.scores_stride) a.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + scores);
   hipError_t e = launch_cache_attend(c, s, cache->codes, cache->dtype, a, stream);
   if (e != hipSuccess) return LTC_ERR_HIP;
+  if (a.scores) return launched(launch_weigh_scores(c, s, a, d_weights, stream));
   switch (cache->codes) {
     case LTC_E4M3: e = launch_weigh<LTC_E4M3>(c, s, cache->dtype, a, d_weights, stream); break;
     case LTC_INT8: e = launch_weigh<LTC_INT8>(c, s, cache->dtype, a, d_weights, stream); break;

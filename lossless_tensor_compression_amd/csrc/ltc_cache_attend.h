@@ -332,18 +332,32 @@ __device__ __forceinline__ void load_queries8(Queries8<D, NC>& q, const AttendAr
   }
 }
 
+// Where a step's scores go besides: nowhere, or to memory, for the positions'
+// weights.  A lane's row has them by position.
+struct NoScores {
+  __device__ __forceinline__ void put(int, int, float4v) const {}
+};
+struct ToScores {
+  float* row;  // null: the lane has no row
+  __device__ __forceinline__ void put(int tv, int b, float4v x) const {
+    if (row) *reinterpret_cast<float4v*>(row + tv + 4 * b) = x;
+  }
+};
+
 // The products of a step to weights: st[nc][b][i] is the one of the token at
 // tv + 4 b + i, sc the scales of the lane's 16 tokens.  edge: some row does not
 // see some token, or it has no page.
-template <int D, int NC>
+template <int D, int NC, class Scores = NoScores>
 __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], float base,
-                                             uint32_t sc, int tv, bool edge, bool have) {
+                                             uint32_t sc, int tv, bool edge, bool have, const Scores& scores = Scores()) {
   const int ke = (int)(sc & 0xff) - 127, we = (int)(sc >> 8) - 127;
   const float wv = (float)we, wh = (float)(we + kHead);
 #pragma unroll
   for (int nc = 0; nc < NC; ++nc) {
     // not 0: hidden scores are -infinity
     const float f = fmaxf(__builtin_amdgcn_ldexpf(base, ke - w.up[nc]), 0x1p-126f);
+    if constexpr (!std::is_same<Scores, NoScores>::value)
+      for (int b = 0; b < 4; ++b) scores.put(tv, b, st[nc][b] * f);
     if (edge) {
       for (int b = 0; b < 4; ++b)
         for (int i = 0; i < 4; ++i) {
@@ -414,9 +428,10 @@ struct OneFactor {
 constexpr int kSpread = 30;
 
 // The products of a step to weights.
-template <int D, int NC, class Eight, class Factor>
+template <int D, int NC, class Eight, class Factor, class Scores = NoScores>
 __device__ __forceinline__ void step_weights4(Rows<D, NC, Eight>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], const Factor& factor_of,
-                                              const Tokens4& of, int tv, bool edge, bool have, bool far) {
+                                              const Tokens4& of, int tv, bool edge, bool have, bool far,
+                                              const Scores& scores = Scores()) {
   const int own = tv & (kStep - 1);
   float4v factor[4], wv[4];
 #pragma unroll
@@ -426,6 +441,8 @@ __device__ __forceinline__ void step_weights4(Rows<D, NC, Eight>& w, float4v (&s
   }
 #pragma unroll
   for (int nc = 0; nc < NC; ++nc) {
+    if constexpr (!std::is_same<Scores, NoScores>::value)
+      for (int b = 0; b < 4; ++b) scores.put(tv, b, st[nc][b] * factor[b]);
     for (int b = 0; b < 4; ++b)
       for (int i = 0; i < 4; ++i) st[nc][b][i] = fmaf(st[nc][b][i], factor[b][i], wv[b][i]);
     if (edge) {
@@ -583,7 +600,8 @@ constexpr int rows_occupancy(int D, int NC, bool four) {
 // at 1,001-6,001 positions (8 heads of 128, 32 query heads) 93 us, 4.6 TB/s, one
 // at 131,071 58 us; by the chain lengths, table, codes, partial results, join
 // where there is not: one at 777 positions 9 us.
-template <int CODES, int D, int NC, int W, bool BF>
+// SCORES: they are written down as well.
+template <int CODES, int D, int NC, int W, bool BF, bool SCORES>
 __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC, CODES == LTC_E2M1)) void k_attend_rows(
     CacheView c, SeqView s, UnitMap map, AttendArgs a, bool bf16, uint32_t units, uint32_t splits, uint32_t per_head) {
   constexpr int R = 16 * NC, KS = D / 32, KL = D / 64, TAIL = D % 64 / 32, DB = D / 16;
@@ -623,6 +641,12 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC, CODES == LTC_E2M1)) v
   const float base = a.scale * kLog2e;
   Rows<D, NC, Eight> w;
   load_rows<CODES, D, NC>(w, a, sp, head, G, r0, packed, bf16, n, g);
+  typename std::conditional<SCORES, ToScores, NoScores>::type scores = {};
+  if constexpr (SCORES) {
+    static_assert(NC == 1, "a lane has one row");
+    const uint32_t r = r0 + n;
+    if (r < packed) scores.row = a.scores + ((uint64_t)(sp.row0 + r / G) * a.q_heads + head * G + r % G) * a.scores_stride;
+  }
   // positions that every row sees need no masks
   const int all_lo = a.window ? max((int)(sp.start + (r1 - 1) / G) + 1 - (int)a.window, 0) : 0;
   const int all_hi = (int)(sp.start + r0 / G) + 1;
@@ -739,11 +763,11 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC, CODES == LTC_E2M1)) v
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      step_weights4(w, st, p, FactorOfTokens{lds_tokens[wave]}, lds_tokens[wave], tv, edge, have_v, far);
+      step_weights4(w, st, p, FactorOfTokens{lds_tokens[wave]}, lds_tokens[wave], tv, edge, have_v, far, scores);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
     } else {
-      step_weights<D, NC>(w, st, p, base, sc, tv, edge, have_v);
+      step_weights<D, NC>(w, st, p, base, sc, tv, edge, have_v, scores);
     }
     // ---- O^T
     if (edge && !kFour) {
@@ -1285,14 +1309,27 @@ inline Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, ui
   return p;
 }
 
+// The numbers between the scores of a row and query head and the next one's where an
+// attention that weighs writes them down: where a wave has 16 rows at most, and the
+// space is not too much.  Reading them again is less than the keys then, and no
+// product: 40 rows at 500-5,000 positions (8 heads of 128, 32 query heads) 53 + 31 us
+// with the products again (k_weigh), 55 + 10 with scores (k_weigh_scores).
+constexpr uint64_t kMostScoreBytes = 1ull << 28;
+inline uint64_t scores_stride(const Plan& p, const CacheView& c, const SeqView& s, uint32_t q_heads) {
+  if (p.tiles || p.nc != 1) return 0;
+  const uint64_t longest = (capacity_of(c, s) + kStep - 1) / kStep * kStep;
+  return longest * s.rows * q_heads * sizeof(float) <= kMostScoreBytes ? longest : 0;
+}
+
 template <int CODES, int D, int W, bool BF>
 hipError_t launch_waves(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
                         hipStream_t st) {
   auto launch = [&](auto kernel) {
     kernel<<<p.grid, 64 * W, 0, st>>>(c, s, p.map, a, bf16, p.units, p.splits, p.per_head);
   };
-  if (p.nc == 1) launch(k_attend_rows<CODES, D, 1, W, BF>);
-  else if constexpr (D <= 192) launch(k_attend_rows<CODES, D, 2, W, BF>);
+  if (p.nc == 1 && a.scores) launch(k_attend_rows<CODES, D, 1, W, BF, true>);
+  else if (p.nc == 1) launch(k_attend_rows<CODES, D, 1, W, BF, false>);
+  else if constexpr (D <= 192) launch(k_attend_rows<CODES, D, 2, W, BF, false>);
   return hipGetLastError();
 }
 

@@ -11,6 +11,10 @@ uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, int codes,
   return p.splits == 1 ? 0 : kCounterBytes + (uint64_t)p.units * c.heads * p.splits * 16 * p.nc * (c.dim + 2) * sizeof(float);
 }
 
+uint64_t cache_scores_stride(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window) {
+  return s.rows ? scores_stride(plan_rows(c, s, q_heads, window, codes == LTC_E2M1), c, s, q_heads) : 0;
+}
+
 hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, int codes, int dtype, const AttendArgs& a,
                                hipStream_t st) {
   const bool bf16 = dtype == LTC_BF16;

@@ -34,17 +34,24 @@ struct AttendArgs {
   float scale;      // of the products before the softmax
   void* ws;
   float* lse;  // [rows][q_heads] log2 of the softmax's sum, or null
+  float* scores;  // [rows][q_heads][scores_stride] in units of log2, by position, or null
+  uint64_t scores_stride;
 };
 
 uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window);
 
+// 0: an attention that weighs does without scores
+uint64_t cache_scores_stride(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window);
+
 hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, int codes, int dtype, const AttendArgs& a,
                                hipStream_t st);
 
-// adds to weights [pages][heads][page] what the rows give the positions they see;
-// a.lse is known
+// add to weights [pages][heads][page] what the rows give the positions they see;
+// a.lse is known, and for the second a.scores
 template <int CODES>
 hipError_t launch_weigh(const CacheView& c, const SeqView& s, int dtype, const AttendArgs& a, float* weights, hipStream_t st);
+
+hipError_t launch_weigh_scores(const CacheView& c, const SeqView& s, const AttendArgs& a, float* weights, hipStream_t st);
 
 struct EvictArgs {
   float* weights;  // [pages][heads][page]

@@ -207,7 +207,7 @@ hipError_t launch_weigh(const CacheView& c, const SeqView& s, int dtype, const A
   const uint64_t steps = (longest + kStep - 1) / kStep, base = (uint64_t)s.seqs * c.heads;
   const uint64_t mean = ((uint64_t)s.rows * (a.q_heads / c.heads) + s.seqs - 1) / s.seqs;  // packed rows of a sequence and head
   const bool share = mean > 64;
-  const uint64_t most = share ? steps : (steps + kWaves - 1) / kWaves, want = ((share ? 4096 : 1024) + base - 1) / base;
+  const uint64_t most = share ? steps : (steps + kWaves - 1) / kWaves, want = ((share ? 4096 : 1536) + base - 1) / base;
   const uint32_t splits = (uint32_t)(want < most ? want : most < 1 ? 1 : most);
   const uint32_t apart = chiplet_share(c.heads);
   const uint32_t per_head = (s.seqs * splits + apart - 1) / apart * apart;
