@@ -334,13 +334,25 @@ __device__ __forceinline__ void load_queries8(Queries8<D, NC>& q, const AttendAr
 
 // Where a step's scores go besides: nowhere, or to memory, for the positions'
 // weights.  A lane's row has them by position.
-struct NoScores {
-  __device__ __forceinline__ void put(int, int, float4v) const {}
-};
+struct NoScores {};
 struct ToScores {
   float* row;  // null: the lane has no row
-  __device__ __forceinline__ void put(int tv, int b, float4v x) const {
-    if (row) *reinterpret_cast<float4v*>(row + tv + 4 * b) = x;
+  // x[b]: of tokens tv + 4 b on.  They change places with those of the other lane
+  // rows, so that a row's 16 neighbouring ones leave in one instruction, a whole line.
+  __device__ __forceinline__ void put(int tv, const float4v (&x)[4]) const {
+    const int g = (threadIdx.x & 63) >> 4;
+    float4v y[4];
+    for (int j = 0; j < 4; ++j) {
+      uint32_t z[4];
+      for (int b = 0; b < 4; ++b) {
+        const float of = x[b][j];  // the cast of the element itself is that of element 0
+        z[b] = __builtin_bit_cast(uint32_t, of);
+      }
+      transpose_rows(z);
+      for (int i = 0; i < 4; ++i) y[i][j] = __builtin_bit_cast(float, z[i]);
+    }
+    if (row)
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<float4v*>(row + tv - 16 * g + 16 * i + 4 * g) = y[i];
   }
 };
 
@@ -356,8 +368,11 @@ __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4
   for (int nc = 0; nc < NC; ++nc) {
     // not 0: hidden scores are -infinity
     const float f = fmaxf(__builtin_amdgcn_ldexpf(base, ke - w.up[nc]), 0x1p-126f);
-    if constexpr (!std::is_same<Scores, NoScores>::value)
-      for (int b = 0; b < 4; ++b) scores.put(tv, b, st[nc][b] * f);
+    if constexpr (!std::is_same<Scores, NoScores>::value) {
+      float4v x[4];
+      for (int b = 0; b < 4; ++b) x[b] = st[nc][b] * f;
+      scores.put(tv, x);
+    }
     if (edge) {
       for (int b = 0; b < 4; ++b)
         for (int i = 0; i < 4; ++i) {
@@ -441,8 +456,11 @@ __device__ __forceinline__ void step_weights4(Rows<D, NC, Eight>& w, float4v (&s
   }
 #pragma unroll
   for (int nc = 0; nc < NC; ++nc) {
-    if constexpr (!std::is_same<Scores, NoScores>::value)
-      for (int b = 0; b < 4; ++b) scores.put(tv, b, st[nc][b] * factor[b]);
+    if constexpr (!std::is_same<Scores, NoScores>::value) {
+      float4v x[4];
+      for (int b = 0; b < 4; ++b) x[b] = st[nc][b] * factor[b];
+      scores.put(tv, x);
+    }
     for (int b = 0; b < 4; ++b)
       for (int i = 0; i < 4; ++i) st[nc][b][i] = fmaf(st[nc][b][i], factor[b][i], wv[b][i]);
     if (edge) {
