@@ -450,91 +450,99 @@ __global__ __launch_bounds__(1024) void k_move(CacheView c, SeqView s, To to, fl
       store_drops<DROPS>(y + 2 * P + slot * DROPS, have ? load_drops<DROPS>(x + 2 * P + off * DROPS) : 0);
     }
   }
-  // ---- keys: 16 bytes of a token at a time
-  for (int j = g; j < PARTS; j += 4) {
-    uint4v x = {0, 0, 0, 0};
-    if (have) x = *reinterpret_cast<const uint4v*>(c.k + src + j * 256 + (off & 15) * 16);
-    if constexpr (!kFour) {
-      if (scale[0] < top[0]) {
-        const float shrink = power_of_two(max(scale[0] - top[0], -126));
-        for (int i = 0; i < 4; ++i) x[i] = to_codes<CODES == LTC_E4M3>(code_values<CODES == LTC_E4M3>(x[i]) * shrink);
-      }
-    }
-    if (live) *reinterpret_cast<uint4v*>(c.k + dst + j * 256 + n * 16) = x;
+  // ---- keys: 16 bytes of a token at a time; loaded here, stored behind the values
+  constexpr int MINE = (PARTS + 3) / 4;
+  uint4v key[MINE];
+#pragma unroll
+  for (int j = 0; j < MINE; ++j) {
+    key[j] = uint4v{0, 0, 0, 0};
+    if (have && 4 * j + g < PARTS) key[j] = *reinterpret_cast<const uint4v*>(c.k + src + (4 * j + g) * 256 + (off & 15) * 16);
   }
   // ---- values: the tokens come in order, so those of one block of 16 follow one
-  // another.  A lane loads 16 bytes of a block (a dim, or two of 4 bits), of four
-  // blocks at a time, takes its tokens' codes out of them one by one, and shifts
-  // each into the new 16 bytes from above.
-  constexpr int LANES = kFour ? D / 2 : D;
+  // another.  A lane loads 16 bytes of a block (a dim, or two of 4 bits) for each of
+  // its dims, of several blocks at a time, takes its tokens' codes out of them one by
+  // one, and shifts each into the new 16 bytes from above.
+  constexpr int LANES = kFour ? D / 2 : D, DIMS = (LANES + 63) / 64, AHEAD = DIMS > 2 ? 4 : 8;
   const uint32_t live_mask = (uint32_t)__ballot(live && g == 0) & 0xffffu;  // the first ones: positions end with -1
   const int tokens = __popc(live_mask);
   const uint32_t here = have ? (old << c.page_log | off) >> 4 : ~0u;  // the block that the token is in
   const uint32_t before = (uint32_t)__shfl_up((int)here, 1);  // asked by all lanes: one that is not asked has nothing to give
   const uint32_t begins = (uint32_t)__ballot(n == 0 || here != before) & live_mask;
   const uint64_t block_at = head_offset(c, have ? old : 0, head) / (kFour ? 2 : 1) + (off >> 4) * block;
-  for (int d = lane; d - lane < LANES; d += 64) {
-    const bool on = d < LANES;
-    uint4v* at = reinterpret_cast<uint4v*>(c.v + dst + d * 16);
-    uint4v x = {0, 0, 0, 0}, kept = {0, 0, 0, 0};
-    if (on && tokens < 16) kept = *at;
-    for (uint32_t left = begins; left;) {
-      uint4v in[4];
-      uint32_t ahead = left;
+  auto shift_in = [](uint4v& x, uint4v from, uint32_t o) {  // code o of 16 bytes into another 16
+    if constexpr (kFour) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = ahead ? __builtin_ctz(ahead) : 0;
-        const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)block_at, t) |
-                              (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(block_at >> 32), t) << 32;
-        in[i] = uint4v{0, 0, 0, 0};
-        if (on && ahead && __builtin_amdgcn_readlane((int)have, t)) in[i] = *reinterpret_cast<const uint4v*>(c.v + base + d * 16);
-        ahead &= ahead - 1;
+      for (int dim = 0; dim < 2; ++dim) {
+        const uint32_t code = (uint32_t)(((uint64_t)from[2 * dim + 1] << 32 | from[2 * dim]) >> (4 * o));
+        x[2 * dim] = __builtin_amdgcn_alignbit(x[2 * dim + 1], x[2 * dim], 4);
+        x[2 * dim + 1] = __builtin_amdgcn_alignbit(code, x[2 * dim + 1], 4);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!left) break;
-        const int t0 = __builtin_ctz(left);
-        left &= left - 1;
-        const int t1 = left ? __builtin_ctz(left) : tokens;
-        for (int t = t0; t < t1; ++t) {
-          const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)off, t) & 15;
-          if constexpr (kFour) {
-#pragma unroll
-            for (int dim = 0; dim < 2; ++dim) {
-              const uint32_t code = (uint32_t)(((uint64_t)in[i][2 * dim + 1] << 32 | in[i][2 * dim]) >> (4 * o));
-              x[2 * dim] = __builtin_amdgcn_alignbit(x[2 * dim + 1], x[2 * dim], 4);
-              x[2 * dim + 1] = __builtin_amdgcn_alignbit(code, x[2 * dim + 1], 4);
-            }
-          } else {
-            const int z = __builtin_amdgcn_readlane(scale[1], t);
-            uint32_t code = o < 8 ? __builtin_amdgcn_perm(in[i][1], in[i][0], o | 0x0c0c0c00u)
-                                  : __builtin_amdgcn_perm(in[i][3], in[i][2], (o - 8) | 0x0c0c0c00u);
-            if (z < top[1])
-              code = to_codes<CODES == LTC_E4M3>(code_values<CODES == LTC_E4M3>(code) * power_of_two(max(z - top[1], -126)));
-            for (int w = 0; w < 3; ++w) x[w] = __builtin_amdgcn_alignbyte(x[w + 1], x[w], 1);
-            x[3] = __builtin_amdgcn_alignbyte(code, x[3], 1);
-          }
-        }
-      }
+    } else {
+      const uint32_t code = o < 8 ? __builtin_amdgcn_perm(from[1], from[0], o | 0x0c0c0c00u)
+                                  : __builtin_amdgcn_perm(from[3], from[2], (o - 8) | 0x0c0c0c00u);
+      for (int w = 0; w < 3; ++w) x[w] = __builtin_amdgcn_alignbyte(x[w + 1], x[w], 1);
+      x[3] = __builtin_amdgcn_alignbyte(code, x[3], 1);
     }
-    if (tokens < 16) {  // down to the first places; those behind stay as they were
-      for (int t = tokens; t < 16; ++t) {
-        if constexpr (kFour) {
-          for (int dim = 0; dim < 2; ++dim) {
-            const uint32_t code = (uint32_t)(((uint64_t)kept[2 * dim + 1] << 32 | kept[2 * dim]) >> (4 * t));
-            x[2 * dim] = __builtin_amdgcn_alignbit(x[2 * dim + 1], x[2 * dim], 4);
-            x[2 * dim + 1] = __builtin_amdgcn_alignbit(code, x[2 * dim + 1], 4);
-          }
-        } else {
-          const uint32_t code = t < 8 ? __builtin_amdgcn_perm(kept[1], kept[0], t | 0x0c0c0c00u)
-                                      : __builtin_amdgcn_perm(kept[3], kept[2], (t - 8) | 0x0c0c0c00u);
-          for (int w = 0; w < 3; ++w) x[w] = __builtin_amdgcn_alignbyte(x[w + 1], x[w], 1);
-          x[3] = __builtin_amdgcn_alignbyte(code, x[3], 1);
-        }
-      }
-    }
-    if (on) *at = x;
+  };
+  uint4v x[DIMS], kept[DIMS];
+#pragma unroll
+  for (int k = 0; k < DIMS; ++k) {
+    x[k] = kept[k] = uint4v{0, 0, 0, 0};
+    if (tokens < 16 && lane + 64 * k < LANES) kept[k] = *reinterpret_cast<const uint4v*>(c.v + dst + (lane + 64 * k) * 16);
   }
+  for (uint32_t left = begins; left;) {
+    uint4v in[AHEAD][DIMS];
+    uint32_t ahead = left;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int t = ahead ? __builtin_ctz(ahead) : 0;
+      const uint64_t base = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)block_at, t) |
+                            (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(block_at >> 32), t) << 32;
+      const bool want = ahead && __builtin_amdgcn_readlane((int)have, t);
+#pragma unroll
+      for (int k = 0; k < DIMS; ++k) {
+        in[i][k] = uint4v{0, 0, 0, 0};
+        if (want && lane + 64 * k < LANES) in[i][k] = *reinterpret_cast<const uint4v*>(c.v + base + (lane + 64 * k) * 16);
+      }
+      ahead &= ahead - 1;
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (!left) break;
+      const int t0 = __builtin_ctz(left);
+      left &= left - 1;
+      const int t1 = left ? __builtin_ctz(left) : tokens;
+      for (int t = t0; t < t1; ++t) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)off, t) & 15;
+#pragma unroll
+        for (int k = 0; k < DIMS; ++k) {
+          shift_in(x[k], in[i][k], o);
+          if constexpr (!kFour) {
+            const int z = __builtin_amdgcn_readlane(scale[1], t);
+            if (z < top[1]) {  // the byte that has just come in, rounded again
+              const float shrink = power_of_two(max(z - top[1], -126));
+              const uint32_t code = to_codes<CODES == LTC_E4M3>(code_values<CODES == LTC_E4M3>(x[k][3] >> 24) * shrink);
+              x[k][3] = (x[k][3] & 0xffffffu) | code << 24;
+            }
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < MINE; ++j) {
+    if constexpr (!kFour) {
+      if (scale[0] < top[0]) {
+        const float shrink = power_of_two(max(scale[0] - top[0], -126));
+        for (int i = 0; i < 4; ++i) key[j][i] = to_codes<CODES == LTC_E4M3>(code_values<CODES == LTC_E4M3>(key[j][i]) * shrink);
+      }
+    }
+    if (live && 4 * j + g < PARTS) *reinterpret_cast<uint4v*>(c.k + dst + (4 * j + g) * 256 + n * 16) = key[j];
+  }
+  for (int t = tokens; t < 16; ++t)  // what lies behind stays as it was
+    for (int k = 0; k < DIMS; ++k) shift_in(x[k], kept[k], (uint32_t)t);
+  for (int k = 0; k < DIMS; ++k)
+    if (lane + 64 * k < LANES) *reinterpret_cast<uint4v*>(c.v + dst + (lane + 64 * k) * 16) = x[k];
 }
 
 template <int CODES> hipError_t launch_move(const CacheView& c, const SeqView& s, const To& to, const EvictArgs& a, hipStream_t st) {
