@@ -573,7 +573,7 @@ int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const l
                      uint32_t window, float scale, void* d_out, void* d_ws, uint64_t ws_nbytes, hipStream_t stream);
 
 /* The same, and what each position was worth to the rows: d_weights, fp32
- * [pages][heads][page], gets at a position's page and token, for each head, the sum
+ * [pages][heads][page] (16-byte aligned), gets at a position's page and token, for each head, the sum
  * of the softmax's weights of all rows that see it and all query heads that read
  * the head, added to what it held; what the positions of the call's own rows held
  * does not count, and positions that no row sees keep what they have.  No two

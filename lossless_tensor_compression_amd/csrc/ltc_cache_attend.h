@@ -290,7 +290,10 @@ __device__ __forceinline__ void load_rows(Rows<D, NC, Eight>& w, const AttendArg
 // operand is 8 bits.  So a query goes in as two E4M3 numbers, q 2^s = high + low /
 // 16 with the row's largest in 2^7..2^8.  high keeps 4 of bf16's 8 bits, rounded,
 // which leaves 4 for low: exact, but for numbers below 2^-13 of the row's largest,
-// which keep 2^-21 of it.  A lane's 32 numbers are dims 16 g .. + 15 and 64 on.
+// which keep 2^-21 of it.  So keys are not turned, and take a quarter of the shared
+// memory: 711 -> 676 us for two prompts of 2,500-4,096 rows of 128 dims, 1,024 -> 869 us
+// of 256 (as the trace has them).  64, 96 and 192 dims would leave a part of each product
+// empty, and fp16's 11 bits would take three numbers.  A lane's 32 numbers are dims 16 g .. + 15 and 64 on.
 typedef int int8v __attribute__((ext_vector_type(8)));
 template <int D, int NC> struct Queries8 {
   int8v part[2][NC][D / 128];  // high, low
@@ -439,7 +442,11 @@ struct OneFactor {
 };
 
 // far: some token's w lies more than kSpread from a first one's, here or in a step
-// before.  Else every weight that counts below the fraction is one above it too.
+// before.  Else they lie within 2 * kSpread of each other, and a weight that is nothing
+// above the fraction (below 2^-126 of the largest, w and all) is one of less than
+// 2^-60 below it.  The usual sum saves the second exponential: with it, and every
+// lane unpacking its own tokens' bytes, two prompts of 2,500-4,096 rows took 895 us,
+// where this took 660.
 constexpr int kSpread = 30;
 
 // The products of a step to weights.
@@ -594,7 +601,9 @@ __device__ __forceinline__ void spoil_rows(const CacheView& c, const AttendArgs&
 // 32 -> 26 us.  3 instead of 2 for one of 128 dims: 64 rows at 1,000-6,000 93 -> 107
 // us, one at 131,071 57 -> 61 us; 2 instead of 1 for 192 dims: 170 -> 207 us.  The
 // most that go without spills else, but for 3 registers of E4M3's two blocks of
-// 128 dims.
+// 128 dims and 18 of 4-bit codes'.  4-bit codes take fewer registers: 2 instead of 1
+// for one block of 192 and 256 dims, with splits to fill them, 64 rows at 1,000-6,000
+// positions of 4 heads 86 -> 47 and 98 -> 58 us; of 16 heads of 64 dims 2 / 3 84 / 75 us.
 constexpr int rows_occupancy(int D, int NC, bool four) {
   return D * NC <= 64 ? 3 : D * NC <= 256 && (four || D < 192) ? 2 : 1;
 }
@@ -990,7 +999,8 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC, CODES == LTC_E2M1)) v
 constexpr uint32_t kTileRows = 128;
 // Workgroups on a CU: as many as registers and shared memory hold.  3 instead
 // of 2 for one prompt of 4,096 rows of 64 dims: 142 -> 115 us; for 2,048 rows of
-// 96 dims registers spill: 64 -> 94 us (for E4M3's 64 dims one does).
+// 96 dims registers spill: 64 -> 94 us (for E4M3's 64 dims one does).  4-bit codes' 64
+// dims, too: two prompts of 2,500-4,096 rows with 2 / 3 565 / 717 us.
 constexpr int tiles_occupancy(int D, bool four) { return D <= 64 && !four ? 3 : D <= 128 ? 2 : 1; }
 
 // The order of a run of 4 * N reads of shared memory and their 4 * N * NC
@@ -1016,7 +1026,9 @@ template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
 // 35% of the time, vector units for 60%; without exp2 it is as fast, without
 // turning 12% faster, without loads 14%, with an eighth of the second product
 // 10%: the chain of a step (read, product, maximum, exp2, product) is longer
-// than two waves a SIMD hide.
+// than two waves a SIMD hide.  4-bit codes: two prompts of 2,500-4,096 rows behind up
+// to 4,096 positions 635 us, 879 TFLOP/s (8-bit ones 650); matrix cores busy for 33%,
+// vector units for 54%.
 template <int CODES, int D, bool BF>
 __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
                                                                           AttendArgs a, bool bf16, uint32_t units,

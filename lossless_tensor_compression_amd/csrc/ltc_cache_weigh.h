@@ -21,7 +21,9 @@ __device__ __forceinline__ float sum_scattered(float (&v)[16], int n) {
   return v[0];
 }
 
-// Waves for each SIMD that the kernel's registers are to leave room for.
+// Waves for each SIMD that the kernel's registers are to leave room for: as many as go
+// without spills (but for 256 dims' one wave where rows are shared).  40 single rows at
+// 500-5,000 positions of 8 heads of 128 dims with 2 / 3: 39 / 34 us.
 constexpr int weigh_occupancy(int D, bool share) { return D <= 128 ? share && D > 64 ? 2 : 3 : D <= 192 || !share ? 2 : 1; }
 
 // A step's keys as they lie in memory.
@@ -55,6 +57,10 @@ template <int CODES, int D> struct RawKeys {
 // the cache's own type.  A lane holds the weights of 16 positions from one row,
 // 2^(x - lse), adds them up over the rows, and at the end 16 lanes' sums are
 // joined.  The order of all sums is fixed.
+//
+// Bound by the vector units: of 16 rows and 64 positions a lane has 16 exponentials and
+// as many multiplications and additions, the matrix cores 4 * D / 32 products.  Two
+// prompts of 1,500-2,100 rows (6 heads of 64, 12 query heads) 46 us.
 //
 // SHARE: a workgroup's waves have the same positions and share the rows out, for
 // prompts; else each wave has every W-th step, for few rows.
@@ -206,7 +212,12 @@ hipError_t launch_weigh(const CacheView& c, const SeqView& s, int dtype, const A
   if (longest > kMaxPositions) longest = kMaxPositions;
   const uint64_t steps = (longest + kStep - 1) / kStep, base = (uint64_t)s.seqs * c.heads;
   const uint64_t mean = ((uint64_t)s.rows * (a.q_heads / c.heads) + s.seqs - 1) / s.seqs;  // packed rows of a sequence and head
-  const bool share = mean > 64;
+  // A workgroup's waves share the rows where there are many for each step, or fewer
+  // steps than waves to fill the chip; else a step's keys are loaded and turned once.
+  // sharing / not: 16 times 32, 64, 128 and 400 packed rows behind 500-5,000 positions
+  // (8 heads of 128) 78 / 21, 79 / 29, 97 / 49 and 66 / 53 us, 6 and 16 prompts of
+  // 8,192 267 / 526 and 650 / 909 us; one of 64 behind 5,000 in 2 heads 4.2 / 6.7 us.
+  const bool share = mean > 1024 || (mean > 16 && base * steps < 4096);
   const uint64_t most = share ? steps : (steps + kWaves - 1) / kWaves, want = ((share ? 4096 : 1536) + base - 1) / base;
   const uint32_t splits = (uint32_t)(want < most ? want : most < 1 ? 1 : most);
   const uint32_t apart = chiplet_share(c.heads);

@@ -9,7 +9,8 @@ constexpr int kWeighLanes = 256, kWeighEach = 4 * kWeighLanes;  // positions of 
 
 // 2^(score - lse), summed over the rows that see a position and the head's query
 // heads, in order.  A lane takes four positions.  Bound by memory: four bytes for
-// each score, eight for each position's weight.
+// each score, eight for each position's weight.  40 rows at 500-5,000 positions (8
+// heads, 32 query heads: 23 MB) 9.7 us.
 __global__ __launch_bounds__(kWeighLanes) void k_weigh_scores(CacheView c, SeqView s, AttendArgs a, float* weights, uint32_t splits) {
   constexpr int AHEAD = 8;  // rows whose scores are in flight
   const uint32_t id = blockIdx.x + gridDim.x * blockIdx.y, split = id % splits, head = id / splits % c.heads;

@@ -73,6 +73,14 @@ def test_window(ltc, codes, dtype, window):
     check(ltc, setup(ltc, 52, 2, 128, 32, codes, dtype, [1, 70, 5, 130], [300, 100, 0, 64]), 4, window)
 
 
+@pytest.mark.parametrize("window", [1, 16, 63, 100, 5000])
+@pytest.mark.parametrize("codes,dtype,dim,page", [("e4m3", BF, 128, 16), ("int8", FP, 64, 64), ("e2m1", BF, 96, 32), ("e2m1", FP, 256, 16)])
+def test_window_of_few_rows(ltc, codes, dtype, dim, page, window):
+    """Rows few enough for their scores to be written down."""
+    check(ltc, setup(ltc, 63, 2, dim, page, codes, dtype, [1, 4, 0, 2, 5], [300, 1100, 17, 0, 64]), 6, window)
+    check(ltc, setup(ltc, 64, 2, dim, page, codes, dtype, [1, 1, 1], [2047, 0, 64], single=True), 2, window)
+
+
 @pytest.mark.parametrize("codes,dtype", TYPES[:3])
 def test_single_rows_again_and_again(ltc, codes, dtype):
     """Without row offsets; calls add up, but for the row's own position."""
@@ -128,8 +136,9 @@ def test_nan_reaches_what_its_row_sees(ltc, codes):
             assert nan[s.table[i, t // 32], 0, t % 32] == (t < bad)
 
 
-def test_bad_pages_and_sequences(ltc):
-    s = Setup4(ltc, 60, 2, 64, 16, BF, [20, 5, 33, 4, 7], [30, 0, 40, 9, 3])
+@pytest.mark.parametrize("new,past", [([20, 5, 33, 4, 7], [30, 0, 40, 9, 3]), ([1, 5, 3, 4, 7], [40, 0, 75, 9, 3])])
+def test_bad_pages_and_sequences(ltc, new, past):
+    s = Setup4(ltc, 60, 2, 64, 16, BF, new, past)
     s.table[0, 2] = -1
     s.table[2, 4] = s.pages
     s.lengths[3] = s.table.shape[1] * 16 + 1
@@ -162,6 +171,28 @@ def test_captured(ltc):
         want = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, weights=b)
         assert torch.equal(out, want) and torch.equal(a, b) and float(a.sum()) > 0
         torch.cuda.synchronize()
+
+
+def test_two_streams_and_two_caches(ltc):
+    """Calls at once on two streams, each with workspaces of its own."""
+    a = Setup4(ltc, 65, 2, 128, 32, BF, [1] * 5, [600, 5, 70, 1000, 31], single=True)
+    q = [a.rows16(8)[0] for _ in range(2)]
+    w = [a.cache.no_weights() for _ in range(2)]
+    want = [ltc.cache_attend(a.cache, q[i], a.gtable, a.glengths, weights=w[i]) for i in range(2)]
+    want_w = [x.clone() for x in w]
+    for x in w:
+        x.zero_()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                w[i].zero_()
+                got.append(ltc.cache_attend(a.cache, q[i], a.gtable, a.glengths, weights=w[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i % 2]) for i, x in enumerate(got))
+    assert all(torch.equal(x, y) for x, y in zip(w, want_w))
 
 
 def test_refusals(ltc):
