@@ -599,7 +599,7 @@ int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, c
  * 65,535 pages at most.  d_lengths [seqs] gets the new lengths, d_positions
  * [seqs][heads][keep] the kept positions, in order and -1 behind the last.
  * Pages of d_to must not be in use: neither named by a table below its length, nor
- * twice here.  What lies behind a sequence's new end in its last page is left.
+ * twice here.  Windows of later attentions count the kept positions.  What lies behind a sequence's new end in its last page is left.
  * 4-bit codes are moved as they are.  An 8-bit page gets the largest scale that one
  * of its tokens had, and codes of smaller scales are divided by the growth and
  * rounded again.  A position without a page has a weight below all numbers; if it is
@@ -622,7 +622,8 @@ int ltc_cache_evict(const ltc_cache* cache, const ltc_cache_seqs* seqs, float* d
  * of the angle position * rate_i; the pairs are dims i and i + rotary / 2, or, with
  * pairs = 1, dims 2 i and 2 i + 1.  d_turns[i] is rate_i / 2 pi, modulo 1, in units of
  * 2^-64, so an angle is exact to 2^-32 of a turn whatever the position (which is
- * below 2^31).  Computed in fp32 and rounded once.
+ * below 2^31).  Computed in fp32 and rounded once: squares and their sum are to stay
+ * within fp32's range (numbers below 1e18 in magnitude, and with eps = 0 above 1e-18).
  * Rows belong to sequences as in the cache's calls (of ltc_cache_seqs the table does
  * not count); lengths count the positions a sequence has come to, which are more than
  * its cache holds once that has been cut.  Rows of no sequence get zeros, and so do

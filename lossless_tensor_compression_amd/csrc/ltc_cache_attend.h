@@ -422,13 +422,14 @@ __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4
 
 // 4-bit codes: every token has scales of its own.  A lane makes of one token's
 // exponents what all lanes need, and finds that of its own 16 tokens in shared
-// memory: [0] log2(e) scale times the keys' scale, [1] w, [2] 2^(-w - kHead).
+// memory: [0] log2(e) scale times the keys' scale, [1] w, [2] 2^-w (2^-126 at least:
+// bytes past 253 are no token's that a row sees, and 0 times an infinity is NaN).
 struct Tokens4 {
   float f[3][kStep];
 };
 __device__ __forceinline__ float key_factor(uint32_t byte, float f) { return f * power_of_two((int)byte - 127); }
 __device__ __forceinline__ float value_exponent(uint32_t byte) { return (float)((int)byte - 127); }
-__device__ __forceinline__ float value_inverse(uint32_t byte) { return power_of_two(127 - kHead - (int)byte); }
+__device__ __forceinline__ float value_inverse(uint32_t byte) { return power_of_two(max(127 - (int)byte, -126)); }
 
 // What the products are multiplied with: a factor for each token, or one for all
 // where the matrix cores have seen to the keys' scales.
@@ -508,7 +509,7 @@ __device__ __forceinline__ void step_weights4(Rows<D, NC, Eight>& w, float4v (&s
         p[nc][b >> 1][(b & 1) * 4 + i] = (_Float16)u;
       }
     }
-    if (!far) w.l[nc] += sum;
+    if (!far) w.l[nc] += sum * power_of_two(-kHead);
   }
 }
 
@@ -1344,7 +1345,7 @@ inline Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, ui
 // space is not too much.  Reading them again is less than the keys then, and no
 // product: 40 rows at 500-5,000 positions (8 heads of 128, 32 query heads) 53 + 31 us
 // with the products again (k_weigh), 55 + 10 with scores (k_weigh_scores).
-constexpr uint64_t kMostScoreBytes = 1ull << 28;
+constexpr uint64_t kMostScoreBytes = 1ull << 27;
 inline uint64_t scores_stride(const Plan& p, const CacheView& c, const SeqView& s, uint32_t q_heads) {
   if (p.tiles || p.nc != 1) return 0;
   const uint64_t longest = (capacity_of(c, s) + kStep - 1) / kStep * kStep;

@@ -302,7 +302,7 @@ def cache_evict(cache, weights, table, lengths, to, keep, recent=0):
     order and with their weights, to the pages that to [sequences, at least
     keep / page] names, whose positions they are from then on: 0 to keep - 1.
     Pages of `to` must not be in use, here or twice; those of table are free
-    afterwards.  A sequence of no more than `keep` positions keeps all of them.
+    afterwards.  Windows of later calls count the kept positions.  A sequence of no more than `keep` positions keeps all of them.
     4-bit codes are moved as they are; a page of 8-bit ones gets the largest
     scale that its tokens had, and codes of smaller scales are rounded again.
 

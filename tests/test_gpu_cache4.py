@@ -198,6 +198,29 @@ def test_attend_query_sizes(ltc, size):
         check_attend4(ltc, s, 4, size=size, scale=1.5)
 
 
+@pytest.mark.parametrize("new,past,group", [([1, 5], [300, 200], 3), ([140], [300], 3), ([300, 9] + [64] * 12, [5] * 14, 8)])
+def test_any_bytes_behind_the_end(ltc, new, past, group):
+    """Exponents of tokens that no row sees, every byte there is."""
+    s = Setup4(ltc, 44, 8 if len(new) > 2 else 1, 64, 64, BF, new, past)
+    for i, n in enumerate(s.lengths):
+        for name in ("ke", "ve"):
+            for h in range(s.H):
+                behind = s.o[name][s.table[i, n // 64], h, n % 64:] if n % 64 else s.o[name][s.free[0], h]
+                behind[:] = s.rng.permutation(np.arange(256 - max(16, len(behind)), 256))[:len(behind)] if i % 2 else s.rng.integers(0, 256, len(behind))
+    s.upload(ltc)
+    check_attend4(ltc, s, s.H * group)
+
+
+@pytest.mark.parametrize("e", [27, 60, 236, 246, 250])
+@pytest.mark.parametrize("new,past,group", [([1, 5], [300, 200], 3), ([300, 9] + [64] * 12, [5] * 14, 8)])
+def test_values_of_any_size(ltc, new, past, group, e):
+    """Value scales near both ends of their range."""
+    s = Setup4(ltc, 45, 8 if len(new) > 2 else 1, 64, 32, BF, new, past)
+    s.o["ve"][:] = s.rng.integers(e - 2 if e > 27 else e, e + 2, s.o["ve"].shape)
+    s.upload(ltc)
+    check_attend4(ltc, s, s.H * group)
+
+
 def test_key_scales_far_from_one(ltc):
     """Keys of 2^80 under queries of 2^-80, and the other way round: the scores
     are ordinary."""
