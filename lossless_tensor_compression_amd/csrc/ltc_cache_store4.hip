@@ -12,7 +12,7 @@ namespace ltc {
 namespace {
 
 // What bounds both: the bytes at memory's rate, and for a few tokens the chain of
-// loads span -> table -> codes.  8 heads of 128: 18,000 tokens written 19.8 us, 4.9
+// loads span -> table -> codes.  8 heads of 128: 18,617 tokens written 19.8 us, 4.9
 // TB/s, where a 1 GiB copy runs at 5.1; a token of each of 48 sequences 5.8 us; 19
 // spans of 20-901 tokens of 5 heads of 96 read 9 us.
 // A workgroup takes a page and head, a wave 16 of its tokens, keys and values

@@ -60,7 +60,7 @@ template <int CODES, int D> struct RawKeys {
 //
 // Bound by the vector units: of 16 rows and 64 positions a lane has 16 exponentials and
 // as many multiplications and additions, the matrix cores 4 * D / 32 products.  Two
-// prompts of 1,500-2,100 rows (6 heads of 64, 12 query heads) 46 us.
+// prompts of 1,500-2,100 rows (6 heads of 64, 12 query heads) 35 us.
 //
 // SHARE: a workgroup's waves have the same positions and share the rows out, for
 // prompts; else each wave has every W-th step, for few rows.
@@ -114,9 +114,10 @@ __global__ __launch_bounds__(64 * W, weigh_occupancy(D, SHARE)) void k_weigh(Cac
     k_page = page_of((at + by) * kStep + kb * 16);
     v_page = page_of((at + by) * kStep + g * 16);
   };
-  if (step * kStep < len) load(step);
+  if (!SHARE && step * kStep < len) load(step);
   for (; step * kStep < len; step += by) {
     const int t0 = step * kStep, tv = t0 + g * 16;
+    if constexpr (SHARE) load(step);  // many rows make up for the wait, and registers are for more waves
     const uint32_t page = now_page;
     const bool have = page < c.pages;
     const int t = tv + n;  // whose weight the lane has in the end
@@ -137,7 +138,7 @@ __global__ __launch_bounds__(64 * W, weigh_occupancy(D, SHARE)) void k_weigh(Cac
     } else {
       by_token[0] = fmaxf(__builtin_amdgcn_ldexpf(f, (int)exps[0] - 127), 0x1p-126f);
     }
-    if ((step + by) * kStep < len) load(step + by);
+    if (!SHARE && (step + by) * kStep < len) load(step + by);
     float sum[16];
     for (int t = 0; t < 16; ++t) sum[t] = 0.0f;
     // the rows at positions from t0 on, and with a window before t0 + 63 + window
@@ -170,8 +171,8 @@ __global__ __launch_bounds__(64 * W, weigh_occupancy(D, SHARE)) void k_weigh(Cac
         }
       const float less = lse;
       // all rows see all of the step's positions, or masks are needed
-      const int first = start + (int)(r0 / G);
-      const bool edge = t0 + kStep > first + 1 || r0 + 16 > rb || window;
+      const int first = start + __builtin_amdgcn_readlane((int)token, 0), last = start + __builtin_amdgcn_readlane((int)token, 15);
+      const bool edge = t0 + kStep > first + 1 || r0 + 16 > rb || (window && t0 + window <= last);
       const int hi = r0 + n < rb ? start + (int)token + 1 : 0, low = window ? hi - window : 0;
       token += token_by;
       qh += qh_by;
@@ -181,14 +182,17 @@ __global__ __launch_bounds__(64 * W, weigh_occupancy(D, SHARE)) void k_weigh(Cac
       }
       if (r0 + R < rb) load_row();
       for (int b = 0; b < 4; ++b)
-        for (int i = 0; i < 4; ++i) {
-          float p = __builtin_amdgcn_exp2f(fmaf(st[b][i], by_token[kFour ? 4 * b + i : 0], -less));
-          if (edge) {
+        for (int i = 0; i < 4; ++i) st[b][i] = fmaf(st[b][i], by_token[kFour ? 4 * b + i : 0], -less);
+      if (edge) {
+        asm volatile("");  // a branch: as selections by `edge` these were most of the loop
+        for (int b = 0; b < 4; ++b)
+          for (int i = 0; i < 4; ++i) {
             const int t = tv + 4 * b + i;
-            p = t < hi && t >= low ? p : 0.0f;
+            st[b][i] = t < hi && t >= low ? st[b][i] : -INFINITY;
           }
-          sum[4 * b + i] += p;
-        }
+      }
+      for (int b = 0; b < 4; ++b)
+        for (int i = 0; i < 4; ++i) sum[4 * b + i] += __builtin_amdgcn_exp2f(st[b][i]);
     }
     float w = sum_scattered(sum, n);
     if constexpr (SHARE) {
@@ -226,7 +230,7 @@ hipError_t launch_weigh(const CacheView& c, const SeqView& s, int dtype, const A
   const dim3 grid((uint32_t)(groups < kGridWidth ? groups : kGridWidth), (uint32_t)((groups + kGridWidth - 1) / kGridWidth));
   return for_numbers(dtype, c.dim, [&](auto type, auto dim) {
     constexpr int DT = decltype(type)::value, D = decltype(dim)::value;
-    constexpr int kShareWaves = D <= 192 ? 8 : 4;
+    constexpr int kShareWaves = 4;
     if (share)
       k_weigh<CODES, DT, D, true, kShareWaves><<<grid, 64 * kShareWaves, 0, st>>>(c, s, a, weights, splits, per_head);
     else

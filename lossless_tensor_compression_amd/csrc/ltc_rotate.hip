@@ -45,7 +45,7 @@ template <int DT> __device__ __forceinline__ void widen8(uint4v x, float (&y)[8]
 // overflow, so far positions lose nothing.  A row's angles are the same for all
 // its heads: each of a wave's lanes makes one or two, while the row's first numbers
 // are on their way, and finds its dims' in shared memory.  (With every lane making
-// its own eight, 15,412 rows of 40 heads took 105 us; 70 us so, 4.5 TB/s, where a 1
+// its own eight, 15,413 rows of 40 heads took 105 us; 70 us so, 4.5 TB/s, where a 1
 // GiB copy runs at 5.1.)  A head's sum of squares goes over its lanes; the numbers
 // that a lane's are turned with come from the lane half of the dims away.
 template <int DT, int D, int W>
@@ -225,7 +225,7 @@ extern "C" int ltc_norm_rotate(const ltc_rotation* rotation, const ltc_cache_seq
   const hipError_t e = for_numbers(rows->dtype, dim, [&](auto type, auto d) {
     constexpr int DT = decltype(type)::value, D = decltype(d)::value;
     // few rows: more waves share one's heads; many, and there are waves enough: fewer
-    // make its angles.  4 / 2 waves: 48 rows of 40 heads 5.1 / 6.5 us, 15,412 of them
+    // make its angles.  4 / 2 waves: 48 rows of 40 heads 5.1 / 6.5 us, 15,413 of them
     // 77 / 70 us.
     if (units <= 1024) k_norm_rotate<DT, D, 4><<<units, 256, 0, stream>>>(s, a);
     else k_norm_rotate<DT, D, 2><<<units, 128, 0, stream>>>(s, a);
