@@ -219,9 +219,9 @@ hipError_t launch_weigh(const CacheView& c, const SeqView& s, int dtype, const A
   // A workgroup's waves share the rows where there are many for each step, or fewer
   // steps than waves to fill the chip; else a step's keys are loaded and turned once.
   // sharing / not: 16 times 32, 64, 128 and 400 packed rows behind 500-5,000 positions
-  // (8 heads of 128) 78 / 21, 79 / 29, 97 / 49 and 66 / 53 us, 6 and 16 prompts of
-  // 8,192 267 / 526 and 650 / 909 us; one of 64 behind 5,000 in 2 heads 4.2 / 6.7 us.
-  const bool share = mean > 1024 || (mean > 16 && base * steps < 4096);
+  // (8 heads of 128) 38 / 19, 43 / 27, 53 / 46 and 40 / 46 us, 6 and 16 prompts of
+  // 8,192 245 / 469 and 621 / 861 us; one of 64 behind 5,000 in 2 heads 4.3 / 6.4 us.
+  const bool share = mean > 256 || (mean > 16 && base * steps < 4096);
   const uint64_t most = share ? steps : (steps + kWaves - 1) / kWaves, want = ((share ? 4096 : 1536) + base - 1) / base;
   const uint32_t splits = (uint32_t)(want < most ? want : most < 1 ? 1 : most);
   const uint32_t apart = chiplet_share(c.heads);
