@@ -559,7 +559,8 @@ int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k
  * (With 4-bit codes read a weight's token for its page.  There, bf16 queries of
  * 128 or 256 dims in calls of many rows enter the products as sums of two E4M3
  * numbers: exactly, but for numbers below 2^-13 of their head's largest, which
- * keep 2^-21 of it.)
+ * keep 2^-21 of it.  Elsewhere bf16 queries meet the codes as they are: they are to
+ * stay below 2^110 in magnitude, and numbers below 2^-110 may count as 0.)
  * A result depends on the call's shapes, not on timing.  The workspace has
  * ltc_cache_attend_workspace_size() bytes, 256-byte aligned (none may be
  * needed, then d_ws may be NULL).  Its first LTC_CACHE_WS_ZEROS bytes must
@@ -579,7 +580,8 @@ int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const l
  * does not count, and positions that no row sees keep what they have.  No two
  * sequences of a call may share a page.  A NaN in a row's output comes with NaN at
  * the positions that the row sees (or, from a NaN among values, with none).
- * Weights below 2^-126 count as 0.  Bad pages and sequences as above; their weights
+ * Weights below 2^-126 count as 0; bf16 queries are to stay below 2^110 in magnitude,
+ * and numbers below 2^-110 may count as 0, whatever the codes.  Bad pages and sequences as above; their weights
  * are left.  d_out is the same as ltc_cache_attend's.  The workspace is one for
  * ltc_cache_attend as well, where it is large enough, and the other way round. */
 uint64_t ltc_cache_attend_weigh_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,

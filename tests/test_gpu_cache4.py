@@ -224,7 +224,7 @@ def test_values_of_any_size(ltc, new, past, group, e):
 def test_key_scales_far_from_one(ltc):
     """Keys of 2^80 under queries of 2^-80, and the other way round: the scores
     are ordinary."""
-    for e, size in ((80, 2.0 ** -80), (-80, 2.0 ** 80)):
+    for e, size in ((80, 2.0 ** -80), (-80, 2.0 ** 80), (100, 2.0 ** -100), (-96, 2.0 ** 100)):
         for new, past in (([1, 3], [90, 200]), ([140], [30])):
             s = Setup4(ltc, 35, 1, 128, 16, BF, new, past)
             for i, n in enumerate(s.lengths):
