@@ -327,10 +327,11 @@ def _rotate(s):
     return one(s["q"], s["q_weight"]), one(s["k"], s["k_weight"])
 
 
-def _least(largest):
-    """The least e with largest <= 6 2^e."""
+def _least(largest, top):
+    """The least e >= LOWEST with largest <= 1.5 top 2^e; top is a power of two."""
     m, e = torch.frexp(largest)
-    return torch.where(m <= 0.75, e - 3, e - 2)
+    e = torch.where(m <= 0.75, e - 1, e) - int(math.log2(top))
+    return torch.where(largest > 0, e, LOWEST).clamp(min=LOWEST)
 
 
 def _write(s):
@@ -348,14 +349,14 @@ def _write(s):
     scales = s["scales"][page]  # [B, pages, H, bytes]
     for kind, name in enumerate(("k", "v")):
         x = s[name].float()[row].movedim(3, 2)  # [B, pages, H, PT, D]
-        largest = x.abs().amax(-1)
-        e = torch.where(largest > 0, _least(largest), LOWEST).clamp(min=LOWEST)
+        e = _least(x.abs().amax(-1), 4.0)
         part = scales[..., kind * PT:(kind + 1) * PT]
         part.copy_(torch.where(fresh[:, :, None], (e + 127).to(torch.uint8), part))
         e = e[..., None]
         if kind == 0:
-            largest = x.unflatten(-1, (-1, 32)).abs().amax(-1)  # [B, pages, H, PT, D/32]
-            drop = torch.where(largest > 0, (e - _least(largest)).clamp(max=15), 15)
+            block = _least(x.unflatten(-1, (-1, 32)).abs().amax(-1), 4.0)  # [B, pages, H, PT, D/32]
+            largest = x.unflatten(-1, (-1, 32)).abs().amax(-1)
+            drop = torch.where(largest > 0, (e - block).clamp(max=15), 15)
             part = scales[..., 2 * PT:].unflatten(-1, (PT, -1))
             nibbles = torch.zeros(*drop.shape[:-1], 2 * part.shape[-1], dtype=torch.uint8, device=x.device)
             nibbles[..., :D // 32] = drop.to(torch.uint8)
