@@ -458,7 +458,8 @@ int ltc_decompress_batch_prof(int count, const void* const* h_headers,
  *   k_codes u8 [pages][heads][page/16][dim/16][16 tokens][16 dims]
  *   v_codes u8 [pages][heads][page/16][dim][16 tokens]
  *   scales  u8 [pages][heads][2] (key, value); a scale is 2^(byte - 127), byte
- *           27..247 (what ltc_cache_write stores: 2^-100 to 2^120)
+ *           27..247 (what ltc_cache_write stores: 2^-100 to 2^120), or less for
+ *           a page of zeros alone
  * Codes are OCP E4M3 (LTC_E4M3) or two's-complement integers (LTC_INT8); a
  * number is its code times its scale.  The layouts are those in which the
  * matrix cores take 16 tokens of keys and values.
@@ -605,7 +606,8 @@ int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, c
  * 4-bit codes are moved as they are.  An 8-bit page gets the largest scale that one
  * of its tokens had, and codes of smaller scales are divided by the growth and
  * rounded again.  A position without a page has a weight below all numbers; if it is
- * kept, it becomes zeros (with the lowest exponents) of weight 0 and is reported, and
+ * kept, it becomes zeros (a page of nothing else gets the lowest scales: bytes of 27,
+ * in 8 bits of 0) of weight 0 and is reported, and
  * so is a page of d_to outside the cache, which is not written.  A sequence whose
  * length is negative or past its table is reported and gets length 0.
  * The workspace, of which none may be needed, is like ltc_cache_attend's, whose zeros

@@ -365,7 +365,9 @@ struct ToScores {
 template <int D, int NC, class Scores = NoScores>
 __device__ __forceinline__ void step_weights(Rows<D, NC>& w, float4v (&st)[NC][4], half8 (&p)[NC][2], float base,
                                              uint32_t sc, int tv, bool edge, bool have, const Scores& scores = Scores()) {
-  const int ke = (int)(sc & 0xff) - 127, we = (int)(sc >> 8) - 127;
+  // a value's byte below the lowest scale is that of a page of zeros, as an eviction
+  // leaves it: 2^127, its inverse, would take the sum past fp32's numbers
+  const int ke = (int)(sc & 0xff) - 127, we = max((int)(sc >> 8) - 127, kLowestScale);
   const float wv = (float)we, wh = (float)(we + kHead);
 #pragma unroll
   for (int nc = 0; nc < NC; ++nc) {
