@@ -578,8 +578,8 @@ int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const l
  * [pages][heads][page] (16-byte aligned), gets at a position's page and token, for each head, the sum
  * of the softmax's weights of all rows that see it and all query heads that read
  * the head, added to what it held; what the positions of the call's own rows held
- * does not count, and positions that no row sees keep what they have.  No two
- * sequences of a call may share a page.  A NaN in a row's output comes with NaN at
+ * does not count, and positions that no row sees are not touched.  No two
+ * sequences of a call may have rows that see positions of the same page.  A NaN in a row's output comes with NaN at
  * the positions that the row sees (or, from a NaN among values, with none).
  * Weights below 2^-126 count as 0; bf16 queries are to stay below 2^110 in magnitude,
  * and numbers below 2^-110 may count as 0, whatever the codes.  Bad pages and sequences as above; their weights

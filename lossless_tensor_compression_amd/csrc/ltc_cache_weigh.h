@@ -122,7 +122,7 @@ __global__ __launch_bounds__(64 * W, weigh_occupancy(D, SHARE)) void k_weigh(Cac
     const bool have = page < c.pages;
     const int t = tv + n;  // whose weight the lane has in the end
     float* at = weights + (((uint64_t)(have ? page : 0) * c.heads + head) << c.page_log) + ((uint32_t)t & page_mask);
-    const bool mine = t < len && have && (!SHARE || wave == 0);
+    const bool mine = t >= lo && t < len && have && (!SHARE || wave == 0);  // what no row sees is not touched
     const float before = mine && t < start ? *at : 0.0f;
     // many rows: the keys are turned into numbers once; few: for each 16 rows again,
     // which leaves registers for more waves

@@ -23,7 +23,8 @@ __global__ __launch_bounds__(kWeighLanes) void k_weigh_scores(CacheView c, SeqVi
   const int lo = window && start + 1 > window ? start + 1 - window : 0;
   const int32_t* table = s.table + seq * s.table_stride;
   const uint64_t first = (uint64_t)sp.row0 * a.q_heads + head * G;
-  for (int t = lo / kWeighEach * kWeighEach + (int)split * kWeighEach + 4 * (int)threadIdx.x; t < len; t += (int)splits * kWeighEach) {
+  // from the first position that a row sees: those before it are not touched
+  for (int t = lo / 4 * 4 + (int)split * kWeighEach + 4 * (int)threadIdx.x; t < len; t += (int)splits * kWeighEach) {
     const uint32_t page = (uint32_t)table[(uint32_t)t >> c.page_log];
     if (page >= c.pages) continue;
     float* at = weights + (((uint64_t)page * c.heads + head) << c.page_log) + ((uint32_t)t & mask);
@@ -48,11 +49,11 @@ __global__ __launch_bounds__(kWeighLanes) void k_weigh_scores(CacheView c, SeqVi
     }
     float4v now;
     for (int j = 0; j < 4; ++j) now[j] = (t + j < start ? before[j] : 0.0f) + sum[j];
-    if (t + 4 <= len) {
+    if (t >= lo && t + 4 <= len) {
       *reinterpret_cast<float4v*>(at) = now;
     } else {
       for (int j = 0; j < 4; ++j)
-        if (t + j < len) at[j] = now[j];
+        if (t + j >= lo && t + j < len) at[j] = now[j];
     }
   }
 }

@@ -260,8 +260,9 @@ def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None, weight
     get what each position is worth to the call's rows added to them: at its
     token's place and each of the cache's heads, the softmax's weights of all
     rows that see it and all query heads that read the head.  Those of the
-    positions that the rows stand for begin at zero.  No two sequences of such a
-    call may share a page."""
+    positions that the rows stand for begin at zero; those that no row sees are
+    not touched.  No two sequences of such a call may have rows that see
+    positions of the same page."""
     if _current_gpu() != cache._index:
         with torch.cuda.device(cache._index):
             return cache_attend(cache, q, table, lengths, cu, window, scale, weights)

@@ -1,0 +1,58 @@
+"""Positions outside the windows of a call's rows: their weights are not
+touched, so their pages may be another sequence's of the same call."""
+import numpy as np
+import pytest
+import torch
+
+import evict_oracle as eo
+from cache4_setup import close
+from gpu_util import banner
+from test_gpu_cache_weigh import BF, FP, setup
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ltc():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    import lossless_tensor_compression_amd as m
+    m.lib()
+    return m
+
+
+@pytest.mark.parametrize("window", [1, 16, 37, 100, 640])
+@pytest.mark.parametrize("codes,dtype,new,past", [("e2m1", BF, [1, 3, 2], [1500, 900, 700]), ("int8", FP, [1, 3, 2], [1500, 900, 700]),
+                                                  ("e4m3", BF, [130, 90, 300], [1500, 900, 700]), ("e2m1", FP, [30, 9, 40], [1500, 900, 700])])
+def test_pages_behind_the_window_are_another_sequence_s(ltc, codes, dtype, new, past, window):
+    """Every entry of a sequence's table that lies before its first row's window
+    names a page of the next sequence, one that its rows see."""
+    banner(f"weigh {codes} {new}, window {window}, stale entries")
+    s = setup(ltc, 82, 2, 64, 16, codes, dtype, new, past)
+    own = s.table.copy()
+    seen = [((n + p - 1) // 16, max(p + 1 - window, 0) // 16) for n, p in zip(new, past)]
+    for i in range(3):
+        last, first = seen[(i + 1) % 3]
+        for j in range(seen[i][1]):
+            s.table[i, j] = own[(i + 1) % 3, last - j % (last - first + 1)]
+    assert all(first >= 3 for _, first in seen)
+    s.gtable = torch.from_numpy(s.table).cuda()
+    w = torch.from_numpy(s.rng.exponential(1.0, tuple(s.cache.no_weights().shape)).astype(np.float32)).cuda()
+    before = w.double().cpu().numpy()
+    q, q64 = s.rows16(6)
+    out = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu, window=window, weights=w)
+    want, slack, shares, off, status = eo.attend(s.o, q64, s.table, s.lengths, s.cu, window)
+    close(out, want, slack, dtype)
+    # the definition, but for positions that no row sees: those keep what they have
+    want_w, slack_w, looked = before.copy(), np.zeros(before.shape), np.zeros(before.shape, bool)
+    for i, (n, p) in enumerate(zip(new, past)):
+        for t in range(max(p + 1 - window, 0), n + p):
+            page, at = s.table[i, t // 16], t % 16
+            assert not looked[page, :, at].any()
+            looked[page, :, at] = True
+            want_w[page, :, at] = (before[page, :, at] if t < p else 0.0) + shares[i][:, t]
+            slack_w[page, :, at] = off[i][:, t] + 2.0 ** -24 * np.abs(want_w[page, :, at])
+    got = w.double().cpu().numpy()
+    assert np.array_equal(got[~looked], before[~looked])
+    assert (np.abs(got - want_w) <= slack_w).all()
+    assert int(s.cache.status.item()) == status == 0
