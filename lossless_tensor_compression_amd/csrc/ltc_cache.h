@@ -129,6 +129,12 @@ LTC_HD Span load_span(const CacheView& c, const SeqView& s, uint32_t seq) {
   return span_of(c0, c1, s.lengths[seq], s.rows, capacity_of(c, s));
 }
 
+// Whether one of the positions [t0, t1) is hidden from one of the rows at positions
+// first .. last.  (t0 + window may pass 2^31.)
+LTC_HD bool some_hidden(int t0, int t1, int first, int last, uint32_t window) {
+  return t1 > first + 1 || (window && last - t0 >= (int)window);
+}
+
 // What a unit loads besides its own sequence's numbers, early and without
 // branches, so that it comes with other loads: the ends of the row offsets, and
 // the numbers of the sequence that it checks (check_sequence).

@@ -172,7 +172,7 @@ __global__ __launch_bounds__(64 * W, weigh_occupancy(D, SHARE)) void k_weigh(Cac
       const float less = lse;
       // all rows see all of the step's positions, or masks are needed
       const int first = start + __builtin_amdgcn_readlane((int)token, 0), last = start + __builtin_amdgcn_readlane((int)token, 15);
-      const bool edge = t0 + kStep > first + 1 || r0 + 16 > rb || (window && t0 + window <= last);
+      const bool edge = r0 + 16 > rb || some_hidden(t0, t0 + kStep, first, last, a.window);
       const int hi = r0 + n < rb ? start + (int)token + 1 : 0, low = window ? hi - window : 0;
       token += token_by;
       qh += qh_by;

@@ -56,3 +56,17 @@ def test_pages_behind_the_window_are_another_sequence_s(ltc, codes, dtype, new, 
     assert np.array_equal(got[~looked], before[~looked])
     assert (np.abs(got - want_w) <= slack_w).all()
     assert int(s.cache.status.item()) == status == 0
+
+
+@pytest.mark.parametrize("codes,dtype,new,past", [("e2m1", BF, [1, 3, 2], [1500, 900, 700]), ("e4m3", BF, [130, 90, 300], [1500, 900, 700]),
+                                                  ("int8", FP, [30, 9, 40], [1500, 900, 700])])
+def test_a_window_wider_than_all_positions_is_none(ltc, codes, dtype, new, past):
+    """The widest that there are: the same numbers as without one."""
+    s = setup(ltc, 83, 2, 64, 16, codes, dtype, new, past)
+    q, _ = s.rows16(6)
+    want = s.cache.no_weights()
+    plain = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu, weights=want)
+    for window in (2 ** 31 - 1, 2 ** 31 - 64, 1 << 30):
+        w = s.cache.no_weights()
+        out = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu, window=window, weights=w)
+        assert torch.equal(out, plain) and torch.equal(w, want) and float(w.sum()) > 0
