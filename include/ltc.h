@@ -625,8 +625,9 @@ int ltc_cache_evict(const ltc_cache* cache, const ltc_cache_seqs* seqs, float* d
  *   (a, b) -> (a cos - b sin, b cos + a sin)
  * of the angle position * rate_i; the pairs are dims i and i + rotary / 2, or, with
  * pairs = 1, dims 2 i and 2 i + 1.  d_turns[i] is rate_i / 2 pi, modulo 1, in units of
- * 2^-64, so an angle is exact to 2^-32 of a turn whatever the position (which is
- * below 2^31).  Computed in fp32 and rounded once: squares and their sum are to stay
+ * 2^-64, so an angle is off by position * 2^-64 of a turn for one in the last place of
+ * its turns (positions are below 2^31), and by 2^-26 of a turn for fp32's 24 bits.
+ * Computed in fp32 and rounded once: squares and their sum are to stay
  * within fp32's range (numbers below 1e18 in magnitude, and with eps = 0 above 1e-18).
  * Rows belong to sequences as in the cache's calls (of ltc_cache_seqs the table does
  * not count); lengths count the positions a sequence has come to, which are more than
