@@ -112,6 +112,8 @@ def norm_rotate(q, k, rotation, lengths, cu=None, q_weight=None, k_weight=None, 
     and rounded once.  Rows that belong to no sequence come out as zeros."""
     gpu = rotation._index
     if _kc._current_gpu() != gpu:
+        if gpu < 0:
+            raise ValueError("the rotation must be on a GPU")
         with torch.cuda.device(gpu):
             return norm_rotate(q, k, rotation, lengths, cu, q_weight, k_weight, eps)
     # straight code from here: it is most of a small call's time

@@ -3,7 +3,9 @@ the library has no part in."""
 from fractions import Fraction
 
 import pytest
+import torch
 
+from lossless_tensor_compression_amd import kv_cache as kc
 from lossless_tensor_compression_amd import rotation as rot
 
 TURN = Fraction("6.28318530717958647692528676655900576839433879875021")  # 2 pi, off by less than 1e-50
@@ -36,3 +38,12 @@ def test_large_rates():
     turns, = rot.turns_of([rate])
     off = (Fraction(turns, 1 << 64) - want + Fraction(1, 2)) % 1 - Fraction(1, 2)
     assert abs(off) <= Fraction(1, 1 << 63)
+
+
+def test_a_rotation_that_is_on_no_gpu(monkeypatch):
+    """Refused, where a search for its GPU would not end."""
+    monkeypatch.setattr(kc, "_current_gpu", lambda: 0)
+    r = rot.Rotation(64, device="cpu")
+    q, lengths = torch.zeros((2, 2, 64), dtype=torch.bfloat16), torch.tensor([3, 4], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        rot.norm_rotate(q, q, r, lengths)
