@@ -599,8 +599,9 @@ int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, c
  * head's kept ones is token j % page of page d_to[i][j / page].  A sequence of no
  * more than `keep` positions is moved whole.  Of seqs the table, the lengths and the
  * number of sequences count (65,535 at most; d_cu NULL, so rows = seqs), and keep is
- * 65,535 pages at most.  d_lengths [seqs] gets the new lengths, d_positions
- * [seqs][heads][keep] the kept positions, in order and -1 behind the last.
+ * 65,535 pages at most.  d_lengths [seqs] gets the new lengths (it may not lie
+ * over those of seqs), d_positions [seqs][heads][keep] the kept positions, in order
+ * and -1 behind the last.
  * Pages of d_to must not be in use: neither named by a table below its length, nor
  * twice here.  Windows of later attentions count the kept positions.  What lies behind a sequence's new end in its last page is left.
  * 4-bit codes are moved as they are.  An 8-bit page gets the largest scale that one

@@ -224,6 +224,9 @@ int ltc_cache_evict(const ltc_cache* cache, const ltc_cache_seqs* seqs, float* d
     return LTC_ERR_INVALID_ARGUMENT;
   const uint64_t need = cache_evict_workspace(c, s);
   if (need && (ws_nbytes < LTC_CACHE_WS_ZEROS + need || !aligned(d_ws, 256))) return LTC_ERR_WORKSPACE;
+  // the workgroups of a sequence's heads read its length when one of them may have written the new one
+  const uintptr_t from = reinterpret_cast<uintptr_t>(s.lengths), to = reinterpret_cast<uintptr_t>(d_lengths);
+  if ((from > to ? from - to : to - from) < s.seqs * sizeof(int32_t)) return LTC_ERR_INVALID_ARGUMENT;
   // behind the bytes that calls leave zero
   uint32_t* ws = need ? reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(d_ws) + LTC_CACHE_WS_ZEROS) : nullptr;
   const EvictArgs a = {d_weights, d_to, to_stride, keep, recent, d_lengths, d_positions, ws};
