@@ -557,12 +557,12 @@ int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k
  * bits down to 2^-23 of the largest weight times its page's value scale
  * (below 2^-34 of it they are lost); scores and sums are held in fp32, and
  * |scale * q k| is to stay below 2^25 (past it weights lose all their bits).
- * (With 4-bit codes read a weight's token for its page.  There, bf16 queries of
- * 128 or 256 dims in calls of many rows enter the products as sums of two E4M3
- * numbers: exactly, but for numbers below 2^-13 of their head's largest, which
- * keep 2^-21 of it.  Elsewhere bf16 queries meet the codes as they are: they are to
- * stay below 2^110 in magnitude, and numbers below 2^-110 may count as 0.)
- * A result depends on the call's shapes, not on timing.  The workspace has
+ * (With 4-bit codes read a weight's token for its page.  There, bf16 queries meet the
+ * codes as they are, but in calls of many rows of 128 or 256 dims as sums of two E4M3
+ * numbers where those leave out at most 2^-16 of the largest of any eight neighbouring
+ * numbers of a query: they are to stay below 2^110 in magnitude, and numbers below
+ * 2^-110 may count as 0.)
+ * A result depends on the call's shapes and numbers, not on timing.  The workspace has
  * ltc_cache_attend_workspace_size() bytes, 256-byte aligned (none may be
  * needed, then d_ws may be NULL).  Its first LTC_CACHE_WS_ZEROS bytes must
  * be zero before the first call that uses it, and every call leaves them

@@ -96,8 +96,8 @@ int check_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_c
 
 // where the rows' sums lie in the workspace of an attention that weighs: behind
 // what the attention uses, and never in the bytes that calls leave zero
-uint64_t lse_offset(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window) {
-  const uint64_t need = cache_attend_workspace(c, s, codes, q_heads, window);
+uint64_t lse_offset(const CacheView& c, const SeqView& s, int codes, int dtype, uint32_t q_heads, uint32_t window) {
+  const uint64_t need = cache_attend_workspace(c, s, codes, dtype, q_heads, window);
   return need < LTC_CACHE_WS_ZEROS ? (uint64_t)LTC_CACHE_WS_ZEROS : (need + 255) / 256 * 256;
 }
 
@@ -147,7 +147,7 @@ uint64_t ltc_cache_attend_workspace_size(const ltc_cache* cache, const ltc_cache
   CacheView c;
   SeqView s;
   if (check_cache(cache, &c) || check_seqs(seqs, &s) || check_heads(c, s, q_heads)) return 0;
-  return cache_attend_workspace(c, s, cache->codes, q_heads, window);
+  return cache_attend_workspace(c, s, cache->codes, cache->dtype, q_heads, window);
 }
 
 int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
@@ -157,7 +157,7 @@ int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const l
   AttendArgs a;
   const int rc = check_attend(cache, seqs, q, q_heads, window, scale, d_out, &c, &s, &a);
   if (rc || !s.rows) return rc;
-  const uint64_t need = cache_attend_workspace(c, s, cache->codes, q_heads, window);
+  const uint64_t need = cache_attend_workspace(c, s, cache->codes, cache->dtype, q_heads, window);
   if (need && (ws_nbytes < need || !aligned(d_ws, 256))) return LTC_ERR_WORKSPACE;
   a.ws = d_ws;
   return launched(launch_cache_attend(c, s, cache->codes, cache->dtype, a, stream));
@@ -169,7 +169,7 @@ uint64_t ltc_cache_attend_weigh_workspace_size(const ltc_cache* cache, const ltc
   SeqView s;
   if (check_cache(cache, &c) || check_seqs(seqs, &s) || check_heads(c, s, q_heads) || !s.rows) return 0;
   const uint64_t stride = cache_scores_stride(c, s, cache->codes, q_heads, window);
-  return scores_offset(s, q_heads, lse_offset(c, s, cache->codes, q_heads, window)) +
+  return scores_offset(s, q_heads, lse_offset(c, s, cache->codes, cache->dtype, q_heads, window)) +
          stride * s.rows * q_heads * sizeof(float);
 }
 
@@ -182,7 +182,7 @@ int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, c
   const int rc = check_attend(cache, seqs, q, q_heads, window, scale, d_out, &c, &s, &a);
   if (rc || !s.rows) return rc;
   if (c.pages && !aligned(d_weights, 16)) return LTC_ERR_INVALID_ARGUMENT;
-  const uint64_t lse = lse_offset(c, s, cache->codes, q_heads, window), scores = scores_offset(s, q_heads, lse);
+  const uint64_t lse = lse_offset(c, s, cache->codes, cache->dtype, q_heads, window), scores = scores_offset(s, q_heads, lse);
   a.scores_stride = cache_scores_stride(c, s, cache->codes, q_heads, window);
   if (ws_nbytes < scores + a.scores_stride * s.rows * q_heads * sizeof(float) || !aligned(d_ws, 256)) return LTC_ERR_WORKSPACE;
   a.ws = d_ws;

@@ -190,7 +190,8 @@ __device__ __forceinline__ Range range_of(const Span& sp, uint32_t tok0, uint32_
 
 // The workspace: kCounters counters, all zero between calls, then the splits'
 // partial results: [unit][head][split][row of the tile] numerators (dim
-// floats), and bound and sum (2 floats) in an array behind them.
+// floats), and bound and sum (2 floats) in an array behind them; or a byte for each
+// tile, [unit][head], that marks those whose queries go in as they are.
 constexpr uint32_t kCounters = 16384;
 constexpr uint64_t kCounterBytes = kCounters * 4;
 
@@ -288,51 +289,70 @@ __device__ __forceinline__ void load_rows(Rows<D, NC, Eight>& w, const AttendArg
 // bf16 queries against keys of 4 bits, 128 dims a product: the matrix cores take
 // the codes as they are, with a scale for each token and 32 dims, if the other
 // operand is 8 bits.  So a query goes in as two E4M3 numbers, q 2^s = high + low /
-// 16 with the row's largest in 2^7..2^8.  high keeps 4 of bf16's 8 bits, rounded,
-// which leaves 4 for low: exact, but for numbers below 2^-13 of the row's largest,
-// which keep 2^-21 of it.  So keys are not turned, and take a quarter of the shared
-// memory: 711 -> 676 us for two prompts of 2,500-4,096 rows of 128 dims, 1,024 -> 869 us
-// of 256 (as the trace has them).  64, 96 and 192 dims would leave a part of each product
-// empty, and fp16's 11 bits would take three numbers.  A lane's 32 numbers are dims 16 g .. + 15 and 64 on.
+// 32 with the row's largest in 2^7..2^8.  high keeps 4 of bf16's 8 bits, rounded,
+// which leaves 4 for low: exact, but for numbers below 2^-14 of the row's largest,
+// which keep 2^-22 of it.  That is nothing beside the row's other numbers, unless one
+// is larger than all others by far and meets keys of zero: rows where it is more than
+// kLeftOut of the largest of some eight neighbours go in as they are, with their tile
+// (the eights of a tile of normal numbers have a largest of 2^-4 of their row's or
+// more).  So keys are not turned, and take a quarter of the shared memory: 711 -> 676
+// us for two prompts of 2,500-4,096 rows of 128 dims, 1,024 -> 869 us of 256 (as the
+// trace has them).  64, 96 and 192 dims would leave a part of each product empty, and
+// fp16's 11 bits would take three numbers.  A lane's 32 numbers are dims 16 g .. + 15
+// and 64 on.
+constexpr float kLeftOut = 0x1p-16f;
 typedef int int8v __attribute__((ext_vector_type(8)));
 template <int D, int NC> struct Queries8 {
   int8v part[2][NC][D / 128];  // high, low
   int scale[2][NC];            // bytes of their exponents
 };
 
+// Returns whether one of the lane's numbers is to go in as it is.
 template <int D, int NC>
-__device__ __forceinline__ void load_queries8(Queries8<D, NC>& q, const AttendArgs& a, const Span& sp, uint32_t head,
+__device__ __forceinline__ bool load_queries8(Queries8<D, NC>& q, const AttendArgs& a, const Span& sp, uint32_t head,
                                               uint32_t G, uint32_t r0, uint32_t packed, int n, int g) {
+  bool far = false;
   for (int nc = 0; nc < NC; ++nc) {
     const uint32_t r = r0 + nc * 16 + n;
     const bool live = r < packed;
     const uint32_t token = live ? r / G : 0, qh = head * G + (live ? r % G : 0);
     const uint16_t* src = a.q.base + (uint64_t)(sp.row0 + token) * a.q.row_stride + (uint64_t)qh * a.q.head_stride;
     uint4v raw[D / 128][4];
-    uint32_t top = 0;
+    uint32_t top = 0, least = 0x7f80;  // the largest number, and the smallest of the largest of eights (of zeros: none)
     for (int j = 0; j < D / 128; ++j)
       for (int i = 0; i < 4; ++i) {
         raw[j][i] = live ? *reinterpret_cast<const uint4v*>(src + j * 128 + i / 2 * 64 + g * 16 + i % 2 * 8) : uint4v{0, 0, 0, 0};
-        for (int w = 0; w < 4; ++w) top = max(top, max(raw[j][i][w] & 0x7fffu, (raw[j][i][w] >> 16) & 0x7fffu));
+        uint32_t of = 0;
+        for (int w = 0; w < 4; ++w) of = max(of, max(raw[j][i][w] & 0x7fffu, (raw[j][i][w] >> 16) & 0x7fffu));
+        top = max(top, of);
+        if (of) least = min(least, of);
       }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    for (int w = 16; w < 64; w <<= 1) {
+      top = max(top, (uint32_t)__shfl_xor((int)top, w));
+      least = min(least, (uint32_t)__shfl_xor((int)least, w));
+    }
     const int up = min(134 - (int)(top >> 7), 122);  // the low part's exponent is a byte, too
     q.scale[0][nc] = 127 - up;
-    q.scale[1][nc] = 123 - up;
-    const float f = power_of_two(up);
+    q.scale[1][nc] = 122 - up;
+    const float f = power_of_two(up), most = widen<LTC_BF16>(least) * f * kLeftOut;
     for (int j = 0; j < D / 128; ++j)
       for (int w = 0; w < 8; ++w) {
         const uint32_t x = raw[j][w / 2][w % 2 * 2], y = raw[j][w / 2][w % 2 * 2 + 1];
         const float4v v = float4v{widen<LTC_BF16>(x & 0xffffu), widen<LTC_BF16>(x >> 16), widen<LTC_BF16>(y & 0xffffu),
                                   widen<LTC_BF16>(y >> 16)} * f;
         const uint32_t high = to_codes<true>(v);
+        const float4v rest = (v - code_values<true>(high)) * 32.0f;
+        const uint32_t low = to_codes<true>(rest);
+        const float4v left = rest - code_values<true>(low);
         q.part[0][nc][j][w] = (int)high;
-        q.part[1][nc][j][w] = (int)to_codes<true>((v - code_values<true>(high)) * 16.0f);
+        q.part[1][nc][j][w] = (int)low;
         // infinities and NaN make the row NaN
         if (top >= 0x7f80u) q.part[0][nc][j][w] = q.part[1][nc][j][w] = 0x7f7f7f7f;
+        else
+          for (int i = 0; i < 4; ++i) far |= fabsf(left[i]) > 32.0f * most;
       }
   }
+  return far;
 }
 
 // Where a step's scores go besides: nowhere, or to memory, for the positions'
@@ -1000,6 +1020,8 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC, CODES == LTC_E2M1)) v
 }
 
 constexpr uint32_t kTileRows = 128;
+// Whether prompts' queries go in as Queries8 where they can.
+constexpr bool may_scale(int codes, int D, bool bf16) { return codes == LTC_E2M1 && bf16 && D % 128 == 0; }
 // Workgroups on a CU: as many as registers and shared memory hold.  3 instead
 // of 2 for one prompt of 4,096 rows of 64 dims: 142 -> 115 us; for 2,048 rows of
 // 96 dims registers spill: 64 -> 94 us (for E4M3's 64 dims one does).  4-bit codes' 64
@@ -1032,7 +1054,13 @@ template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
 // than two waves a SIMD hide.  4-bit codes: two prompts of 2,500-4,096 rows behind up
 // to 4,096 positions 635 us, 879 TFLOP/s (8-bit ones 650); matrix cores busy for 33%,
 // vector units for 54%.
-template <int CODES, int D, bool BF>
+//
+// SCALED: Queries8, but for the tiles with a row that is to go in as it is: those get a
+// mark in the workspace, and a second launch without SCALED takes them.  Both ways in
+// one kernel share its registers, and spill 26 of 128 dims' and 109 of 256's.  The
+// second launch takes 4 us where nothing is marked (two prompts of 2,500-4,096 rows 639
+// -> 643 us).
+template <int CODES, int D, bool BF, bool SCALED>
 __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
                                                                           AttendArgs a, bool bf16, uint32_t units,
                                                                           uint32_t per_head) {
@@ -1040,7 +1068,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
   constexpr bool kFour = CODES == LTC_E2M1;
   constexpr uint32_t kBlockBytes = kFour ? 8 * D : 16 * D;
   constexpr int VB = kFour ? DB / 2 : DB, VL = (VB + 3) / 4;
-  constexpr bool kScaled = kFour && BF && D % 128 == 0;  // Queries8
+  constexpr bool kScaled = SCALED, kMarked = may_scale(CODES, D, BF);
   typedef typename std::conditional<kScaled, NoQueries, typename std::conditional<kFour && BF, bf8, half8>::type>::type Eight;
   constexpr int KX = kScaled ? D / 128 : KS;        // the first product's instructions for a block
   __shared__ half8 lds[2][(KX * 4 + DB * 2) * 64];  // keys [x][b][lane], values [i][h][lane]
@@ -1053,6 +1081,9 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
   uint32_t head, unit, split;
   place(blockIdx.x + gridDim.x * blockIdx.y, c.heads, 1, per_head, &head, &unit, &split);
   if (head >= c.heads || unit >= units) return;
+  uint8_t* mark = static_cast<uint8_t*>(a.ws) + kCounterBytes + (uint64_t)unit * c.heads + head;
+  if constexpr (kMarked && !kScaled)
+    if (!*mark) return;
   const uint32_t G = a.q_heads / c.heads;
   uint32_t seq;
   Span sp;
@@ -1063,6 +1094,7 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
   if (none.n) clear_unnamed(none, a.out + (uint64_t)head * G * D, (uint64_t)a.q_heads * D, G * D, unit, units);
   if (!(sp.ok && check_sequence(c, s, early)) && threadIdx.x == 0) report(c, kCacheBadSeq);
   const uint32_t packed = sp.n * G;
+  if (kScaled && threadIdx.x == 0) *mark = 0;
   if (!mine || own * R >= packed) return;
   const uint32_t r0 = (uint32_t)own * R, r1 = min(r0 + R, packed);
   Range rg = range_of(sp, r0 / G, (r1 - 1) / G + 1, a.window, 1, 1);
@@ -1079,7 +1111,16 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
   Rows<D, NC, Eight> w;
   load_rows<CODES, D, NC>(w, a, sp, head, G, w0, packed, bf16, n, g);
   Queries8<kScaled ? D : 128, NC> q8;
-  if constexpr (kScaled) load_queries8<D, NC>(q8, a, sp, head, G, w0, packed, n, g);
+  if constexpr (kScaled) {
+    __shared__ bool lds_far[4];
+    const bool far = __any(load_queries8<D, NC>(q8, a, sp, head, G, w0, packed, n, g));
+    if (lane == 0) lds_far[wave] = far;
+    __syncthreads();
+    if (lds_far[0] || lds_far[1] || lds_far[2] || lds_far[3]) {
+      if (threadIdx.x == 0) *mark = 1;
+      return;
+    }
+  }
 
   const uint32_t page_mask = (1u << c.page_log) - 1;
   const int kb = n >> 2;
@@ -1370,7 +1411,9 @@ template <int CODES, int D, bool BF>
 hipError_t launch_rows(const CacheView& c, const SeqView& s, bool bf16, const AttendArgs& a, const Plan& p,
                        hipStream_t st) {
   if (p.tiles) {
-    k_attend_tiles<CODES, D, BF><<<p.grid, 256, 0, st>>>(c, s, p.map, a, bf16, p.units, p.per_head);
+    auto launch = [&](auto kernel) { kernel<<<p.grid, 256, 0, st>>>(c, s, p.map, a, bf16, p.units, p.per_head); };
+    if constexpr (may_scale(CODES, D, BF)) launch(k_attend_tiles<CODES, D, BF, true>);
+    launch(k_attend_tiles<CODES, D, BF, false>);
     return hipGetLastError();
   }
   // Heads of 192 and 256 dims leave a SIMD one wave: where nothing is split, two

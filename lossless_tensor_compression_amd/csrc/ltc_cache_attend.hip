@@ -5,9 +5,10 @@ namespace ltc {
 
 template hipError_t launch_attend<LTC_E4M3>(const CacheView&, const SeqView&, bool, const AttendArgs&, hipStream_t);
 
-uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window) {
+uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, int codes, int dtype, uint32_t q_heads, uint32_t window) {
   if (!s.rows) return 0;
   const Plan p = plan_rows(c, s, q_heads, window, codes == LTC_E2M1);
+  if (p.tiles) return may_scale(codes, (int)c.dim, dtype == LTC_BF16) ? kCounterBytes + (uint64_t)p.units * c.heads : 0;  // marks
   return p.splits == 1 ? 0 : kCounterBytes + (uint64_t)p.units * c.heads * p.splits * 16 * p.nc * (c.dim + 2) * sizeof(float);
 }
 

@@ -38,7 +38,7 @@ struct AttendArgs {
   uint64_t scores_stride;
 };
 
-uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window);
+uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, int codes, int dtype, uint32_t q_heads, uint32_t window);
 
 // 0: an attention that weighs does without scores
 uint64_t cache_scores_stride(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window);
