@@ -135,6 +135,19 @@ LTC_HD bool some_hidden(int t0, int t1, int first, int last, uint32_t window) {
   return t1 > first + 1 || (window && last - t0 >= (int)window);
 }
 
+// Scores that an attention writes down, for each row and query head: those of the
+// positions from score_first on, which is in order for the sequence's first row and a
+// step's first; scores_length holds them whatever the lengths are.
+constexpr uint32_t kScoreStep = 64;
+LTC_HD uint32_t score_first(uint32_t start, uint32_t window) {
+  const uint32_t first = window && start + 1 > window ? start + 1 - window : 0;
+  return first / kScoreStep * kScoreStep;
+}
+LTC_HD uint64_t scores_length(uint64_t capacity, uint32_t rows, uint32_t window) {
+  const uint64_t seen = (uint64_t)window + rows + 2 * kScoreStep, most = window && seen < capacity ? seen : capacity;
+  return (most + kScoreStep - 1) / kScoreStep * kScoreStep;
+}
+
 // What a unit loads besides its own sequence's numbers, early and without
 // branches, so that it comes with other loads: the ends of the row offsets, and
 // the numbers of the sequence that it checks (check_sequence).

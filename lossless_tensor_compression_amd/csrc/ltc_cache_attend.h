@@ -168,7 +168,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
 
 // The positions that a tile of packed rows looks at, in steps of kStep, and
 // how they are shared out: split i takes steps [i * per, (i + 1) * per).
-constexpr int kStep = 64;
+constexpr int kStep = (int)kScoreStep;
 struct Range {
   int lo, hi;            // positions [lo, hi) that some row sees
   int first, steps;      // steps first .. first + steps cover them
@@ -359,7 +359,7 @@ __device__ __forceinline__ bool load_queries8(Queries8<D, NC>& q, const AttendAr
 // weights.  A lane's row has them by position.
 struct NoScores {};
 struct ToScores {
-  float* row;  // null: the lane has no row
+  float* row;  // where position 0's would be; null: the lane has no row
   // x[b]: of tokens tv + 4 b on.  They change places with those of the other lane
   // rows, so that a row's 16 neighbouring ones leave in one instruction, a whole line.
   __device__ __forceinline__ void put(int tv, const float4v (&x)[4]) const {
@@ -695,7 +695,9 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC, CODES == LTC_E2M1)) v
   if constexpr (SCORES) {
     static_assert(NC == 1, "a lane has one row");
     const uint32_t r = r0 + n;
-    if (r < packed) scores.row = a.scores + ((uint64_t)(sp.row0 + r / G) * a.q_heads + head * G + r % G) * a.scores_stride;
+    if (r < packed)
+      scores.row = a.scores + ((uint64_t)(sp.row0 + r / G) * a.q_heads + head * G + r % G) * a.scores_stride -
+                   score_first(sp.start, a.window);
   }
   // positions that every row sees need no masks
   const int all_lo = a.window ? max((int)(sp.start + (r1 - 1) / G) + 1 - (int)a.window, 0) : 0;
@@ -1389,9 +1391,9 @@ inline Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, ui
 // product: 40 rows at 500-5,000 positions (8 heads of 128, 32 query heads) 53 + 31 us
 // with the products again (k_weigh), 55 + 10 with scores (k_weigh_scores).
 constexpr uint64_t kMostScoreBytes = 1ull << 27;
-inline uint64_t scores_stride(const Plan& p, const CacheView& c, const SeqView& s, uint32_t q_heads) {
+inline uint64_t scores_stride(const Plan& p, const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
   if (p.tiles || p.nc != 1) return 0;
-  const uint64_t longest = (capacity_of(c, s) + kStep - 1) / kStep * kStep;
+  const uint64_t longest = scores_length(capacity_of(c, s), s.rows, window);
   return longest * s.rows * q_heads * sizeof(float) <= kMostScoreBytes ? longest : 0;
 }
 

@@ -13,7 +13,7 @@ uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, int codes,
 }
 
 uint64_t cache_scores_stride(const CacheView& c, const SeqView& s, int codes, uint32_t q_heads, uint32_t window) {
-  return s.rows ? scores_stride(plan_rows(c, s, q_heads, window, codes == LTC_E2M1), c, s, q_heads) : 0;
+  return s.rows ? scores_stride(plan_rows(c, s, q_heads, window, codes == LTC_E2M1), c, s, q_heads, window) : 0;
 }
 
 hipError_t launch_cache_attend(const CacheView& c, const SeqView& s, int codes, int dtype, const AttendArgs& a,

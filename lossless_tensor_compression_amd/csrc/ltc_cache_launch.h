@@ -34,7 +34,7 @@ struct AttendArgs {
   float scale;      // of the products before the softmax
   void* ws;
   float* lse;  // [rows][q_heads] log2 of the softmax's sum, or null
-  float* scores;  // [rows][q_heads][scores_stride] in units of log2, by position, or null
+  float* scores;  // [rows][q_heads][scores_stride] in units of log2, by position from score_first on, or null
   uint64_t scores_stride;
 };
 

@@ -22,6 +22,7 @@ __global__ __launch_bounds__(kWeighLanes) void k_weigh_scores(CacheView c, SeqVi
   const int start = (int)sp.start, len = (int)sp.len, window = (int)a.window;
   const int lo = window && start + 1 > window ? start + 1 - window : 0;
   const int32_t* table = s.table + seq * s.table_stride;
+  const int from = (int)score_first(sp.start, a.window);
   const uint64_t first = (uint64_t)sp.row0 * a.q_heads + head * G;
   // from the first position that a row sees: those before it are not touched
   for (int t = lo / 4 * 4 + (int)split * kWeighEach + 4 * (int)threadIdx.x; t < len; t += (int)splits * kWeighEach) {
@@ -37,7 +38,7 @@ __global__ __launch_bounds__(kWeighLanes) void k_weigh_scores(CacheView c, SeqVi
       for (int i = 0; i < AHEAD; ++i) {
         const uint32_t r = min(r0 + i, rows - 1);
         const uint64_t row = first + (uint64_t)(r / G) * a.q_heads + r % G;
-        x[i] = *reinterpret_cast<const float4v*>(a.scores + row * a.scores_stride + t);
+        x[i] = *reinterpret_cast<const float4v*>(a.scores + row * a.scores_stride + (t - from));
         lse[i] = a.lse[row];
       }
 #pragma unroll

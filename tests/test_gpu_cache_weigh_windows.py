@@ -7,7 +7,7 @@ import torch
 import evict_oracle as eo
 from cache4_setup import close
 from gpu_util import banner
-from test_gpu_cache_weigh import BF, FP, setup
+from test_gpu_cache_weigh import BF, FP, check, setup
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,14 @@ def test_a_window_wider_than_all_positions_is_none(ltc, codes, dtype, new, past)
         w = s.cache.no_weights()
         out = ltc.cache_attend(s.cache, q, s.gtable, s.glengths, s.gcu, window=window, weights=w)
         assert torch.equal(out, plain) and torch.equal(w, want) and float(w.sum()) > 0
+
+
+@pytest.mark.parametrize("window", [1, 5, 64, 100, 1024])
+@pytest.mark.parametrize("codes,dtype,dim", [("e2m1", BF, 128), ("int8", FP, 64), ("e4m3", BF, 96)])
+def test_scores_of_wide_tables(ltc, codes, dtype, dim, window):
+    """Tables of far more positions than the windows: rows' scores begin with what the sequence's first row sees."""
+    s = setup(ltc, 84, 2, dim, 16, codes, dtype, [1, 4, 0, 2, 5, 1], [4000, 1100, 17, 0, 64, 63])
+    table = s.rng.integers(-5, s.pages + 5 if codes == "e2m1" else 5, (6, 9000)).astype(np.int32)
+    table[:, :s.table.shape[1]] = s.table
+    s.table, s.gtable = table, torch.from_numpy(table).cuda()
+    check(ltc, s, 6, window)
