@@ -584,7 +584,10 @@ int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const l
  * Weights below 2^-126 count as 0; bf16 queries are to stay below 2^110 in magnitude,
  * and numbers below 2^-110 may count as 0, whatever the codes.  Bad pages and sequences as above; their weights
  * are left.  d_out is the same as ltc_cache_attend's.  The workspace is one for
- * ltc_cache_attend as well, where it is large enough, and the other way round. */
+ * ltc_cache_attend as well, where it is large enough, and the other way round; it has
+ * 4 bytes more for each row and query head, and in calls of few rows their scores, 4
+ * bytes for each position that the table has room for (with a window: about window +
+ * rows), if those are 2^27 bytes at most. */
 uint64_t ltc_cache_attend_weigh_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,
                                                uint32_t window);
 int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,

@@ -12,7 +12,8 @@ back, attended to in place, and cut to the positions that were worth most.
 A binding over ltc_cache_write, ltc_cache_read, ltc_cache_attend,
 ltc_cache_attend_weigh and ltc_cache_evict of include/ltc.h, where the layouts, the rounding and what happens with bad
 tables are written down.  Calls run on the current stream, allocate nothing
-but their outputs and a workspace that the cache keeps for each stream, and
+but their outputs and a workspace, which a GPU's caches keep together for each
+stream (attention with weights of few rows wants up to 128 MiB, others a few), and
 never synchronise, so they can be captured in a graph.  They have no backward
 pass: rows that require a gradient are refused.  Threads may share a
 cache; their calls on one stream run in the order in which they are made.
@@ -26,6 +27,7 @@ table[i, t // page].  table, lengths and cu are int32 tensors on the GPU.
 import ctypes
 import struct
 import threading
+import weakref
 
 import torch
 
@@ -45,6 +47,17 @@ _current_gpu = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() builds a Stream object: 2.7 us a call
 _pack_seqs = struct.Struct("=QQQQIIII").pack      # ltc_cache_seqs
 _pack_rows = struct.Struct("=QQQ").pack           # ltc_cache_rows
+
+
+_lock = threading.Lock()  # from a workspace's lookup to the launch that uses it
+_workspaces = weakref.WeakValueDictionary()  # (GPU, stream) -> the workspace that its caches share
+
+
+def _room(need):
+    """Bytes of a workspace of at least `need`: a power of two, and from 16 MiB on the next eighth of one."""
+    bits = (need - 1).bit_length()
+    step = 1 << (bits if bits <= 24 else bits - 4)
+    return -(-need // step) * step
 
 
 class CacheStruct(ctypes.Structure):
@@ -105,7 +118,7 @@ class KVCache:
         self._ref = ctypes.byref(self._struct)
         self._index = self.device.index
         self._workspaces = {}  # stream -> tensor, its first bytes zero between calls
-        self._lock = threading.Lock()  # from a workspace's lookup to the launch that uses it
+        self._lock = _lock
 
     @staticmethod
     def _shape(k_codes, v_codes, scales, codes):
@@ -163,16 +176,19 @@ class KVCache:
 
     def _workspace(self, need, stream):
         """A workspace for a call on the stream, for the caller to hold until
-        it has launched.  Each stream keeps one, since its calls run in order;
-        a captured call gets its own, which lives and is cleared with the
-        graph."""
+        it has launched.  A stream's calls run in order, so each stream keeps
+        one, for all caches of the GPU; a captured call gets its own, which
+        lives and is cleared with the graph."""
         captured = torch._C._cuda_isCurrentStreamCapturing()
         ws = None if captured else self._workspaces.get(stream)
+        if ws is not None and ws.numel() >= need:
+            return ws
+        ws = None if captured else _workspaces.get((self._index, stream))
         if ws is None or ws.numel() < need:
-            ws = torch.empty(1 << (need - 1).bit_length(), dtype=torch.uint8, device=self.device)
+            ws = torch.empty(_room(need), dtype=torch.uint8, device=self.device)
             ws[:WS_ZEROS].zero_()
-            if not captured:
-                self._workspaces[stream] = ws
+        if not captured:
+            self._workspaces[stream] = _workspaces[self._index, stream] = ws
         return ws
 
     def _seqs(self, table, lengths, cu, rows):
