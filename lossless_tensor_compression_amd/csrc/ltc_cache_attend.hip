@@ -3,6 +3,9 @@
 
 namespace ltc {
 
+// built in files of their own
+extern template hipError_t launch_attend<LTC_INT8>(const CacheView&, const SeqView&, bool, const AttendArgs&, hipStream_t);
+extern template hipError_t launch_attend<LTC_E2M1>(const CacheView&, const SeqView&, bool, const AttendArgs&, hipStream_t);
 template hipError_t launch_attend<LTC_E4M3>(const CacheView&, const SeqView&, bool, const AttendArgs&, hipStream_t);
 
 uint64_t cache_attend_workspace(const CacheView& c, const SeqView& s, int codes, int dtype, uint32_t q_heads, uint32_t window) {
