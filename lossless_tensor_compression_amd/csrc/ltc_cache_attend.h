@@ -295,9 +295,8 @@ __device__ __forceinline__ void load_rows(Rows<D, NC, Eight>& w, const AttendArg
 // is larger than all others by far and meets keys of zero: rows where it is more than
 // kLeftOut of the largest of some eight neighbours go in as they are, with their tile
 // (the eights of a tile of normal numbers have a largest of 2^-4 of their row's or
-// more).  So keys are not turned, and take a quarter of the shared memory: 711 -> 676
-// us for two prompts of 2,500-4,096 rows of 128 dims, 1,024 -> 869 us of 256 (as the
-// trace has them).  64, 96 and 192 dims would leave a part of each product empty, and
+// more).  So keys are not turned, and take a quarter of the shared memory: 670 -> 643
+// us for two prompts of 2,500-4,096 rows of 128 dims, 1,036 -> 888 us of 256.  64, 96 and 192 dims would leave a part of each product empty, and
 // fp16's 11 bits would take three numbers.  A lane's 32 numbers are dims 16 g .. + 15
 // and 64 on.
 constexpr float kLeftOut = 0x1p-16f;
@@ -334,7 +333,8 @@ __device__ __forceinline__ bool load_queries8(Queries8<D, NC>& q, const AttendAr
     const int up = min(134 - (int)(top >> 7), 122);  // the low part's exponent is a byte, too
     q.scale[0][nc] = 127 - up;
     q.scale[1][nc] = 122 - up;
-    const float f = power_of_two(up), most = widen<LTC_BF16>(least) * f * kLeftOut;
+    const float f = power_of_two(up);
+    float gone = 0.0f;  // the most that is left out, times 32
     for (int j = 0; j < D / 128; ++j)
       for (int w = 0; w < 8; ++w) {
         const uint32_t x = raw[j][w / 2][w % 2 * 2], y = raw[j][w / 2][w % 2 * 2 + 1];
@@ -348,9 +348,9 @@ __device__ __forceinline__ bool load_queries8(Queries8<D, NC>& q, const AttendAr
         q.part[1][nc][j][w] = (int)low;
         // infinities and NaN make the row NaN
         if (top >= 0x7f80u) q.part[0][nc][j][w] = q.part[1][nc][j][w] = 0x7f7f7f7f;
-        else
-          for (int i = 0; i < 4; ++i) far |= fabsf(left[i]) > 32.0f * most;
+        for (int i = 0; i < 4; ++i) gone = fmaxf(gone, fabsf(left[i]));
       }
+    far |= top < 0x7f80u && gone > 32.0f * kLeftOut * (widen<LTC_BF16>(least) * f);
   }
   return far;
 }
@@ -1061,7 +1061,8 @@ template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
 // mark in the workspace, and a second launch without SCALED takes them.  Both ways in
 // one kernel share its registers, and spill 26 of 128 dims' and 109 of 256's.  The
 // second launch takes 4 us where nothing is marked (two prompts of 2,500-4,096 rows 639
-// -> 643 us).
+// -> 643 us, two of 256 dims 870 -> 888: compared number by number, not by the largest that
+// is left out, 917).
 template <int CODES, int D, bool BF, bool SCALED>
 __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
                                                                           AttendArgs a, bool bf16, uint32_t units,
