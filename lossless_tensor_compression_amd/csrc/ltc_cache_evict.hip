@@ -561,8 +561,11 @@ template <int CODES> hipError_t launch_move(const CacheView& c, const SeqView& s
 }
 
 // One workgroup a sequence and head, or several where that leaves most of the chip
-// idle and there are positions to share: a sequence of 65,537 in 4 heads with 1 / 16
-// of them 60 / 27 us.
+// idle and there are positions to share, as the table has room for them.  One / several
+// for cuts to 256 of 60,000 positions (of 64 dims): 4 sequences and heads 48 / 28 us, 32
+// of them 48 / 35, 64 54 / 54, 128 63 / 97, 512 140 / 341 us.  Of 9,000 positions 4 and
+// 64 of them 17 / 25 and 17 / 30 us, of 1,000 in tables of 131,072 13 / 23 and 13 / 39
+// us: there several are too many, and the host does not see the lengths.
 uint32_t pick_splits(const CacheView& c, const SeqView& s) {
   const uint64_t pairs = (uint64_t)s.seqs * c.heads, capacity = capacity_of(c, s);
   if (pairs > 64 || capacity <= 2 * kRound) return 0;
