@@ -296,7 +296,7 @@ __device__ __forceinline__ void load_rows(Rows<D, NC, Eight>& w, const AttendArg
 // kLeftOut of the largest of some eight neighbours go in as they are, with their tile
 // (the eights of a tile of normal numbers have a largest of 2^-4 of their row's or
 // more).  So keys are not turned, and take a quarter of the shared memory: 670 -> 643
-// us for two prompts of 2,500-4,096 rows of 128 dims, 1,036 -> 888 us of 256.  64, 96 and 192 dims would leave a part of each product empty, and
+// us for two prompts of 2,500-4,096 rows of 128 dims, 1,036 -> 899 us of 256.  64, 96 and 192 dims would leave a part of each product empty, and
 // fp16's 11 bits would take three numbers.  A lane's 32 numbers are dims 16 g .. + 15
 // and 64 on.
 constexpr float kLeftOut = 0x1p-16f;
@@ -471,6 +471,11 @@ struct OneFactor {
 // lane unpacking its own tokens' bytes, two prompts of 2,500-4,096 rows took 895 us,
 // where this took 660.
 constexpr int kSpread = 30;
+// A token that no row sees does not count, so that a result does not go one way or the
+// other by what lies behind a sequence's end: k_attend_rows leaves it out (64 rows at
+// 1,001-6,001 positions 63.5 -> 64.5 us; as below 66.8), k_attend_tiles takes the nearest one
+// that some row sees in its place (two prompts of 2,500-4,096 rows 643 -> 642 us; as before 655).
+__device__ __forceinline__ int seen_token(int t, const Range& rg) { return min(max(t, rg.lo), rg.hi - 1); }
 
 // The products of a step to weights.
 template <int D, int NC, class Eight, class Factor, class Scores = NoScores>
@@ -777,8 +782,9 @@ __global__ __launch_bounds__(64 * W, rows_occupancy(D, NC, CODES == LTC_E2M1)) v
       to.f[0][lane] = key_factor(exps[0], base * power_of_two(-kLift));
       to.f[1][lane] = value_exponent(exps[1]);
       to.f[2][lane] = value_inverse(exps[1]);
-      if (first_w < 0) first_w = __builtin_amdgcn_readfirstlane((int)exps[1]);
-      far = far || __any(abs((int)exps[1] - first_w) > kSpread);
+      const uint64_t seen = __ballot(t0 + lane >= rg.lo && t0 + lane < rg.hi && have_v);
+      if (first_w < 0 && seen) first_w = __builtin_amdgcn_readlane((int)exps[1], __builtin_ctzll(seen));
+      far = far || (__ballot(abs((int)exps[1] - first_w) > kSpread) & seen) != 0;
     }
     // ---- S^T
     float4v st[NC][4];
@@ -1147,19 +1153,19 @@ __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_
   uint32_t scales = 0, next_scales = 0;
   auto pages = [&](int step) {
     k_page = page_of(step * kStep + kb * 16);
-    v_page = page_of(step * kStep + g * 16);
+    v_page = kFour ? table[(uint32_t)seen_token(step * kStep + g * 16, rg) >> c.page_log] : page_of(step * kStep + g * 16);
   };
   auto load = [&](int step) {
     const uint8_t* k = c.k + block_at(step * kStep + kb * 16, k_page) + (n & 3) * 16 + wave * 64;
     const uint8_t* v = c.v + block_at(step * kStep + g * 16, v_page) + n * 16;
     if constexpr (kFour) {
-      const int tk = step * kStep + kb * 16, tv = step * kStep + g * 16;
+      const int tk = step * kStep + kb * 16, tv = seen_token(step * kStep + lane, rg);  // of the exponents
       const uint8_t* sk = c.scales + token_scales(c, (uint32_t)k_page < c.pages ? (uint32_t)k_page : 0, head);
       const uint8_t* sv = c.scales + token_scales(c, (uint32_t)v_page < c.pages ? (uint32_t)v_page : 0, head);
       kq.load(k, sk + 2 * (page_mask + 1) + (((uint32_t)tk & page_mask) + (n & 3) + 4 * wave) * drop_bytes(D), g);
       if constexpr (kScaled) key_exp = sk[((uint32_t)tk & page_mask) + (n & 3) + 4 * wave];
-      else exps[0] = sv[((uint32_t)tv & page_mask) + n];
-      exps[1] = sv[((uint32_t)tv & page_mask) + n + page_mask + 1];
+      else exps[0] = sv[(uint32_t)tv & page_mask];
+      exps[1] = sv[((uint32_t)tv & page_mask) + page_mask + 1];
     } else {
       for (int j = 0; j < KL; ++j) kr[j] = *reinterpret_cast<const uint4v*>(k + g * 256 + j * 1024);
       if constexpr (TAIL) kt = *reinterpret_cast<const uint2v*>(k + KL * 1024 + (g >> 1) * 256 + (g & 1) * 8);
