@@ -12,6 +12,7 @@ stream, allocate nothing but their outputs and never synchronise.  They have no
 backward pass: tensors that require a gradient are refused.
 """
 import ctypes
+import functools
 import math
 import struct
 
@@ -30,6 +31,7 @@ class RotationStruct(ctypes.Structure):
                 ("rotary", ctypes.c_uint32), ("pairs", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
 
 
+@functools.lru_cache(maxsize=None)
 def _pi(bits):
     """pi * 2^bits, to the nearest few, by Machin's formula: 16 arctan(1/5) - 4 arctan(1/239)."""
     def arctan_of_inverse(n):
@@ -53,7 +55,7 @@ def turns_of(rates):
         if not math.isfinite(r):
             raise ValueError(f"rate {r}")
         n, d = float(r).as_integer_ratio()
-        bits = 160 + n.bit_length()
+        bits = 160 + (n.bit_length() + 63) // 64 * 64  # few different ones
         out.append((n << (63 + bits)) // (d * _pi(bits)) % (1 << 64))
     return out
 
