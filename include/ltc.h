@@ -560,7 +560,7 @@ int ltc_cache_read(const ltc_cache* cache, const ltc_cache_seqs* seqs, void* d_k
  * (With 4-bit codes read a weight's token for its page.  There, bf16 queries meet the
  * codes as they are, but in calls of many rows of 128 or 256 dims as sums of two E4M3
  * numbers where those leave out at most 2^-16 of the largest of any eight neighbouring
- * numbers of a query: they are to stay below 2^110 in magnitude, and numbers below
+ * numbers of a query: they are to stay below 2^107 in magnitude, and numbers below
  * 2^-110 may count as 0.)
  * A result depends on the call's shapes and numbers, not on timing.  The workspace has
  * ltc_cache_attend_workspace_size() bytes, 256-byte aligned (none may be
@@ -575,19 +575,24 @@ int ltc_cache_attend(const ltc_cache* cache, const ltc_cache_seqs* seqs, const l
                      uint32_t window, float scale, void* d_out, void* d_ws, uint64_t ws_nbytes, hipStream_t stream);
 
 /* The same, and what each position was worth to the rows: d_weights, fp32
- * [pages][heads][page] (16-byte aligned), gets at a position's page and token, for each head, the sum
- * of the softmax's weights of all rows that see it and all query heads that read
- * the head, added to what it held; what the positions of the call's own rows held
- * does not count, and positions that no row sees are not touched.  No two
- * sequences of a call may have rows that see positions of the same page.  A NaN in a row's output comes with NaN at
- * the positions that the row sees (or, from a NaN among values, with none).
- * Weights below 2^-126 count as 0; bf16 queries are to stay below 2^110 in magnitude,
- * and numbers below 2^-110 may count as 0, whatever the codes.  Bad pages and sequences as above; their weights
- * are left.  d_out is the same as ltc_cache_attend's.  The workspace is one for
- * ltc_cache_attend as well, where it is large enough, and the other way round; it has
- * 4 bytes more for each row and query head, and in calls of few rows their scores, 4
- * bytes for each position that the table has room for (with a window: about window +
- * rows), if those are 2^27 bytes at most. */
+ * [pages][heads][page] (16-byte aligned), gets at a position's page and token, for
+ * each head, the sum of the softmax's weights of all rows that see it and all query
+ * heads that read the head, added to what it held; what the positions of the call's
+ * own rows held does not count, and positions that no row sees are not touched.  No
+ * two sequences of a call may have rows that see positions of the same page.  (So a
+ * page that is handed out anew need not be cleared, unless its new positions' rows are
+ * attended to without weights: what is there then counts later.)
+ * A NaN in a row's output comes with NaN at the positions that the row sees (or, from
+ * a NaN among values, with none).  Weights below 2^-126 count as 0, and scores are held
+ * in fp32: a weight is off by about 2^-22 of its row's largest score, of itself.  bf16
+ * queries are to stay below 2^110 in magnitude (over 4-bit codes 2^107), and numbers
+ * below 2^-110 may count as 0, whatever the codes.  Bad pages and sequences as above;
+ * their weights are left, and what is added where offsets decrease is not defined.
+ * d_out is the same as ltc_cache_attend's.  The workspace is one for ltc_cache_attend
+ * as well, where it is large enough, and the other way round; it has 4 bytes more for
+ * each row and query head and, in calls of few rows, for each of their scores (of the
+ * positions that the table has room for; with a window of about window + rows), if
+ * those are 2^27 bytes at most. */
 uint64_t ltc_cache_attend_weigh_workspace_size(const ltc_cache* cache, const ltc_cache_seqs* seqs, uint32_t q_heads,
                                                uint32_t window);
 int ltc_cache_attend_weigh(const ltc_cache* cache, const ltc_cache_seqs* seqs, const ltc_cache_rows* q, uint32_t q_heads,
