@@ -10,8 +10,8 @@ back, attended to in place, and cut to the positions that were worth most.
                                                  the positions of most weight to other pages
 
 A binding over ltc_cache_write, ltc_cache_read, ltc_cache_attend,
-ltc_cache_attend_weigh and ltc_cache_evict of include/ltc.h, where the layouts, the rounding and what happens with bad
-tables are written down.  Calls run on the current stream, allocate nothing
+ltc_cache_attend_weigh and ltc_cache_evict of include/ltc.h, where the layouts,
+the rounding and what happens with bad tables are written down.  Calls run on the current stream, allocate nothing
 but their outputs and a workspace, which a GPU's caches keep together for each
 stream (attention with weights of few rows wants up to 128 MiB, others a few), and
 never synchronise, so they can be captured in a graph.  They have no backward
@@ -278,7 +278,9 @@ def cache_attend(cache, q, table, lengths, cu=None, window=0, scale=None, weight
     rows that see it and all query heads that read the head.  Those of the
     positions that the rows stand for begin at zero; those that no row sees are
     not touched.  No two sequences of such a call may have rows that see
-    positions of the same page."""
+    positions of the same page.  Where rows are attended to without weights,
+    their positions keep what the page's earlier tokens had: clear those of a
+    page that is handed out anew then."""
     if _current_gpu() != cache._index:
         with torch.cuda.device(cache._index):
             return cache_attend(cache, q, table, lengths, cu, window, scale, weights)
@@ -319,7 +321,8 @@ def cache_evict(cache, weights, table, lengths, to, keep, recent=0):
     order and with their weights, to the pages that to [sequences, at least
     keep / page] names, whose positions they are from then on: 0 to keep - 1.
     Pages of `to` must not be in use, here or twice; those of table are free
-    afterwards.  Windows of later calls count the kept positions.  A sequence of no more than `keep` positions keeps all of them.
+    afterwards.  Windows of later calls count the kept positions.  A sequence of
+    no more than `keep` positions keeps all of them.
     4-bit codes are moved as they are; a page of 8-bit ones gets the largest
     scale that its tokens had, and codes of smaller scales are rounded again.
 

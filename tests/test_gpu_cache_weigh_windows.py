@@ -81,3 +81,17 @@ def test_scores_of_wide_tables(ltc, codes, dtype, dim, window):
     table[:, :s.table.shape[1]] = s.table
     s.table, s.gtable = table, torch.from_numpy(table).cuda()
     check(ltc, s, 6, window)
+
+
+def test_positions_that_came_without_weights(ltc):
+    """What their page's earlier tokens left counts, unless it is cleared."""
+    s = setup(ltc, 85, 2, 64, 16, "e4m3", BF, [1, 1], [60, 33], single=True)
+    q, _ = s.rows16(4)
+    alone = s.cache.no_weights()
+    ltc.cache_attend(s.cache, q, s.gtable, s.glengths, weights=alone)
+    stale = torch.full_like(alone, 2.0)
+    ltc.cache_attend(s.cache, q, s.gtable, s.glengths, weights=stale)
+    for i, n in enumerate((61, 34)):
+        for t in range(n):
+            at = int(s.table[i, t // 16]), slice(None), t % 16
+            assert torch.equal(stale[at], alone[at] + (2.0 if t < n - 1 else 0.0))
