@@ -294,11 +294,11 @@ __device__ __forceinline__ void load_rows(Rows<D, NC, Eight>& w, const AttendArg
 // which keep 2^-22 of it.  That is nothing beside the row's other numbers, unless one
 // is larger than all others by far and meets keys of zero: rows where it is more than
 // kLeftOut of the largest of some eight neighbours go in as they are, with their tile
-// (the eights of a tile of normal numbers have a largest of 2^-4 of their row's or
-// more).  So keys are not turned, and take a quarter of the shared memory: 670 -> 643
-// us for two prompts of 2,500-4,096 rows of 128 dims, 1,036 -> 899 us of 256.  64, 96 and 192 dims would leave a part of each product empty, and
-// fp16's 11 bits would take three numbers.  A lane's 32 numbers are dims 16 g .. + 15
-// and 64 on.
+// (it can be where the row's largest is 2^6 times that; in a tile of normal numbers it
+// is 2^4 times).  So keys are not turned, and take a quarter of the shared memory: 670 ->
+// 643 us for two prompts of 2,500-4,096 rows of 128 dims, 1,036 -> 888 us of 256.  64, 96
+// and 192 dims would leave a part of each product empty, and fp16's 11 bits would take
+// three numbers.  A lane's 32 numbers are dims 16 g .. + 15 and 64 on.
 constexpr float kLeftOut = 0x1p-16f;
 typedef int int8v __attribute__((ext_vector_type(8)));
 template <int D, int NC> struct Queries8 {
@@ -1060,15 +1060,15 @@ template <int N, int NC> __device__ __forceinline__ void reads_ahead() {
 // turning 12% faster, without loads 14%, with an eighth of the second product
 // 10%: the chain of a step (read, product, maximum, exp2, product) is longer
 // than two waves a SIMD hide.  4-bit codes: two prompts of 2,500-4,096 rows behind up
-// to 4,096 positions 635 us, 879 TFLOP/s (8-bit ones 650); matrix cores busy for 33%,
-// vector units for 54%.
+// to 4,096 positions 640 us, 873 TFLOP/s (8-bit ones 650; fp16 queries 675); matrix cores
+// busy for 37%, vector units for 56%.
 //
 // SCALED: Queries8, but for the tiles with a row that is to go in as it is: those get a
 // mark in the workspace, and a second launch without SCALED takes them.  Both ways in
 // one kernel share its registers, and spill 26 of 128 dims' and 109 of 256's.  The
 // second launch takes 4 us where nothing is marked (two prompts of 2,500-4,096 rows 639
 // -> 643 us, two of 256 dims 870 -> 888: compared number by number, not by the largest that
-// is left out, 917).
+// is left out, 917).  Where all tiles are, those prompts take 679 and 1,038 us.
 template <int CODES, int D, bool BF, bool SCALED>
 __global__ __launch_bounds__(256, tiles_occupancy(D, CODES == LTC_E2M1)) void k_attend_tiles(CacheView c, SeqView s, UnitMap map,
                                                                           AttendArgs a, bool bf16, uint32_t units,
@@ -1395,8 +1395,8 @@ inline Plan plan_rows(const CacheView& c, const SeqView& s, uint32_t q_heads, ui
 // The numbers between the scores of a row and query head and the next one's where an
 // attention that weighs writes them down: where a wave has 16 rows at most, and the
 // space is not too much.  Reading them again is less than the keys then, and no
-// product: 40 rows at 500-5,000 positions (8 heads of 128, 32 query heads) 53 + 31 us
-// with the products again (k_weigh), 55 + 10 with scores (k_weigh_scores).
+// product: 40 rows at 500-5,000 positions (8 heads of 128, 32 query heads) 52 + 30 us
+// with the products again (k_weigh), 62 + 9 with scores (k_weigh_scores).
 constexpr uint64_t kMostScoreBytes = 1ull << 27;
 inline uint64_t scores_stride(const Plan& p, const CacheView& c, const SeqView& s, uint32_t q_heads, uint32_t window) {
   if (p.tiles || p.nc != 1) return 0;

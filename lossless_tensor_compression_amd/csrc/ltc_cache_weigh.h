@@ -58,9 +58,10 @@ template <int CODES, int D> struct RawKeys {
 // 2^(x - lse), adds them up over the rows, and at the end 16 lanes' sums are
 // joined.  The order of all sums is fixed.
 //
-// Bound by the vector units: of 16 rows and 64 positions a lane has 16 exponentials and
-// as many multiplications and additions, the matrix cores 4 * D / 32 products.  Two
-// prompts of 1,500-2,100 rows (6 heads of 64, 12 query heads) 35 us.
+// Bound by the vector units and by what they wait for: two prompts of 1,500-2,100 rows
+// (6 heads of 64, 12 query heads, a window of 1,600) 35 us, in half of which a vector
+// instruction issues, 103 for 16 rows and 64 positions, 16 of them exponentials; matrix
+// cores are busy for 16%.
 //
 // SHARE: a workgroup's waves have the same positions and share the rows out, for
 // prompts; else each wave has every W-th step, for few rows.
