@@ -42,12 +42,13 @@ template <int DT> __device__ __forceinline__ void widen8(uint4v x, float (&y)[8]
 // A workgroup takes a row, its waves the heads in turn, 64 / (D / 8) at a time,
 // queries' and keys' in one list.  An angle is a number of turns in 64 bits of
 // fraction: the position times the turns of one position, modulo 1 by the product's
-// overflow, so far positions lose nothing but what fp32 does of any (2^-26 of a turn).  A row's angles are the same for all
-// its heads: each of a wave's lanes makes one or two, while the row's first numbers
-// are on their way, and finds its dims' in shared memory.  (With every lane making
-// its own eight, 15,413 rows of 40 heads took 105 us; 70 us so, 4.5 TB/s, where a 1
-// GiB copy runs at 5.1.)  A head's sum of squares goes over its lanes; the numbers
-// that a lane's are turned with come from the lane half of the dims away.
+// overflow, so far positions lose nothing but what fp32 does of any (2^-26 of a turn).
+// A row's angles are the same for all its heads: each of a wave's lanes makes one or
+// two, while the row's first numbers are on their way, and finds its dims' in shared
+// memory.  (With every lane making its own eight, 15,413 rows of 40 heads took 105 us;
+// 70 us so, 4.5 TB/s, where a 1 GiB copy runs at 5.1.)  A head's sum of squares goes
+// over its lanes; the numbers that a lane's are turned with come from the lane half of
+// the dims away.
 template <int DT, int D, int W>
 __global__ __launch_bounds__(64 * W) void k_norm_rotate(SeqView s, RotateArgs a) {
   constexpr int L = D / 8, HEADS = 64 / L, AHEAD = 3;

@@ -11,12 +11,13 @@ back, attended to in place, and cut to the positions that were worth most.
 
 A binding over ltc_cache_write, ltc_cache_read, ltc_cache_attend,
 ltc_cache_attend_weigh and ltc_cache_evict of include/ltc.h, where the layouts,
-the rounding and what happens with bad tables are written down.  Calls run on the current stream, allocate nothing
-but their outputs and a workspace, which a GPU's caches keep together for each
-stream (attention with weights of few rows wants up to 128 MiB, others a few), and
-never synchronise, so they can be captured in a graph.  They have no backward
-pass: rows that require a gradient are refused.  Threads may share a
-cache; their calls on one stream run in the order in which they are made.
+the rounding and what happens with bad tables are written down.  Calls run on
+the current stream, allocate nothing but their outputs and a workspace, which a
+GPU's caches keep together for each stream (attention with weights of few rows
+wants up to 128 MiB, others a few), and never synchronise, so they can be
+captured in a graph.  They have no backward pass: rows that require a gradient
+are refused.  Threads may share a cache; their calls on one stream run in the
+order in which they are made.
 
 Rows cu[i]..cu[i+1] of a call belong to sequence i and stand for its last
 positions, lengths[i] - (cu[i+1] - cu[i]) to lengths[i] - 1; without cu each
